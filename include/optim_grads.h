@@ -1,0 +1,77 @@
+/*
+ * optim_grads.h -- C ABI of the operators on gradients around the optimizer
+ * step of optim_step.h: norms of every tensor of a list and of the whole,
+ * clipping where the gradients lie, and the weight gradients of a mixture of
+ * experts.  The conventions of optim_step.h hold for every entry point here
+ * (status codes, ownership, streams, graph capture); in addition
+ * optim_clip_grads and optim_expert_grad write gradients.
+ */
+#ifndef OPTIM_GRADS_H
+#define OPTIM_GRADS_H
+
+#include "optim_step.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* ---- gradient lists -----------------------------------------------------
+ * A plan of algorithm OPTIM_ALGO_GRADS holds the gradients of a list and
+ * nothing else: numel, grad and grad_dtype of optim_tensor_list are read
+ * (grad_dtype F32, BF16 or F16; arrays aligned to their element size, any
+ * tensor may begin anywhere in a bucket), every other pointer is ignored and
+ * may be NULL.  It is made, traced and destroyed as every plan
+ * (optim_plan_create, optim_plan_create_static, ...); opts may be NULL, and
+ * tile, grid, state_dtype and state_layout must be 0 in it.  No two tensors
+ * may overlap.  The calls of one plan must not overlap each other (they
+ * share its workspace).
+ * The steps, optim_check_finite and optim_grad_norm refuse such a plan
+ * (OPTIM_EINVAL); optim_grad_norms does both of the latter.                */
+
+/* Norms: square root of the sum of squares, sum of magnitudes, largest
+ * magnitude.                                                              */
+enum { OPTIM_NORM_L2 = 0, OPTIM_NORM_L1 = 1, OPTIM_NORM_INF = 2 };
+
+/* The norm of every tensor of the list and of the whole list, of the
+ * unscaled gradients g = G * s, s = *inv_scale_dev (NULL: 1), in one read of
+ * the gradients:
+ *   norms_dev[i] = ||g_i||   (float[n]; 0 for an empty tensor; may be NULL)
+ *   *total_dev   = ||(g_1, ..., g_n)||, from the unrounded sums
+ *   *coef_dev    = s * min(1, max_norm / (total + 1e-6))   (may be NULL)
+ * max_norm <= 0 or +inf: no clipping (coef = s); NaN is OPTIM_EINVAL.
+ * found_inf_dev (may be NULL) is set to 1.0f if any element is NaN or +-Inf
+ * and left unchanged otherwise, as by optim_check_finite; the norms of the
+ * tensors concerned and the total are then not finite, and coef = s.
+ * Sums are kept in fp64 in an order fixed by the list, so results repeat bit
+ * for bit; a finite list has finite norms (up to fp32's range), and
+ * gradients whose squares leave fp32's range at either end are summed
+ * exactly.                                                                 */
+int optim_grad_norms(optim_plan *plan, int32_t kind, const float *inv_scale_dev,
+                     double max_norm, float *found_inf_dev, float *norms_dev,
+                     float *total_dev, float *coef_dev, void *stream);
+
+/* One norm over several lists (a model stepped by two algorithms), or over
+ * the ranks of a sharded one (their totals gathered into one array): from
+ * norms_dev[count], norms of the unscaled gradients of disjoint lists,
+ *   *total_dev = their norm of the same kind,
+ *   *coef_dev  = s * min(1, max_norm / (total + 1e-6)), s = *inv_scale_dev.
+ * Rules for max_norm and a total that is not finite as in optim_grad_norms.
+ * total_dev may be an element of norms_dev; count 0 gives total 0.
+ * total_dev or coef_dev may be NULL.                                      */
+int optim_clip_coef(const float *norms_dev, int64_t count, int32_t kind,
+                    const float *inv_scale_dev, double max_norm,
+                    float *total_dev, float *coef_dev, void *stream);
+
+/* G <- G * *coef_dev in every gradient of the list, the product in fp32,
+ * rounded once to the gradient's type (nearest even).  Nothing is read or
+ * written where *coef_dev is 1, or where found_inf_dev is given and
+ * *found_inf_dev is not 0 (the step that follows is skipped).  With the coef
+ * of optim_grad_norms the gradients are then unscaled and clipped: the step
+ * that follows takes inv_scale NULL.                                      */
+int optim_clip_grads(optim_plan *plan, const float *coef_dev,
+                     const float *found_inf_dev, void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* OPTIM_GRADS_H */

@@ -57,7 +57,9 @@ enum {
     OPTIM_ALGO_BLOCKWISE = 3,
     OPTIM_ALGO_BLOCKWISE_ADEMAMIX = 4,
     OPTIM_ALGO_LION = 5,
-    OPTIM_ALGO_LAMB = 6
+    OPTIM_ALGO_LAMB = 6,
+    OPTIM_ALGO_MUON = 7, /* matrices, stepped by optim_muon.h              */
+    OPTIM_ALGO_GRADS = 8 /* gradients alone, for optim_grads.h             */
 };
 /* Adam-mini partition of a tensor ([MINI], AdamWMini constructor/step). */
 enum { OPTIM_MINI_FULL_V = 0, OPTIM_MINI_HEAD = 1, OPTIM_MINI_SCALAR = 2 };

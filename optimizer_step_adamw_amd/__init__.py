@@ -3,7 +3,8 @@ for AMD Instinct MI355X (gfx950).
 
 Argument marshalling only: torch tensors are turned into device pointers and a
 HIP stream handle; every step of the computation runs in the library's HIP
-kernels.  Functions keep the C names of ``include/optim_step.h``.  If the
+kernels.  Functions keep the C names of ``include/optim_step.h`` and
+``include/optim_grads.h``.  If the
 library has not been built, importing the binding works but every call raises
 ``RuntimeError`` -- there is no fallback path.
 """
@@ -20,7 +21,8 @@ OPTIM_EINVAL, OPTIM_EALIGN, OPTIM_EDTYPE, OPTIM_EWORKSPACE, OPTIM_EUNSUPPORTED, 
 OPTIM_F32, OPTIM_BF16, OPTIM_F16 = 0, 1, 2
 OPTIM_LAYOUT_SEPARATE, OPTIM_LAYOUT_INTERLEAVED = 0, 1
 (OPTIM_ALGO_ADAMW, OPTIM_ALGO_ADEMAMIX, OPTIM_ALGO_ADAM_MINI, OPTIM_ALGO_BLOCKWISE,
- OPTIM_ALGO_BLOCKWISE_ADEMAMIX, OPTIM_ALGO_LION, OPTIM_ALGO_LAMB) = range(7)
+ OPTIM_ALGO_BLOCKWISE_ADEMAMIX, OPTIM_ALGO_LION, OPTIM_ALGO_LAMB, OPTIM_ALGO_MUON, OPTIM_ALGO_GRADS) = range(9)
+OPTIM_NORM_L2, OPTIM_NORM_L1, OPTIM_NORM_INF = range(3)
 OPTIM_MINI_FULL_V, OPTIM_MINI_HEAD, OPTIM_MINI_SCALAR = range(3)
 OPTIM_SCHED_NONE, OPTIM_SCHED_COSINE = 0, 1
 
@@ -33,6 +35,8 @@ EXPORTED = (
     "optim_step_8bit_blockwise_ademamix", "optim_step_lion", "optim_step_lamb",
     "optim_plan_create_static", "optim_plan_trace", "optim_plan_trace_read",
 )
+# entry points of include/optim_grads.h
+EXPORTED_GRADS = ("optim_grad_norms", "optim_clip_coef", "optim_clip_grads")
 # bytes of the library's static per-device workspace (optim_plan_create_static)
 OPTIM_STATIC_WORKSPACE_BYTES = 16 << 20
 
@@ -127,6 +131,9 @@ def lib() -> ctypes.CDLL:
                                                     _P, _P, _P], i32),
             "optim_step_lion": ([_P, ctypes.POINTER(optim_lion_hp), _P, _P, _P, _P, _P], i32),
             "optim_step_lamb": ([_P, ctypes.POINTER(optim_adamw_hp), _P, _P, _P, _P, _P], i32),
+            "optim_grad_norms": ([_P, i32, _P, f64, _P, _P, _P, _P, _P], i32),
+            "optim_clip_coef": ([_P, i64, i32, _P, f64, _P, _P, _P], i32),
+            "optim_clip_grads": ([_P, _P, _P, _P], i32),
         }
         for name, (args, res) in sigs.items():
             fn = getattr(L, name)
@@ -205,6 +212,18 @@ class TensorList:
             s.head_numel = ctypes.cast(self._hn, ctypes.POINTER(ctypes.c_int64))
         s.param_dtype, s.grad_dtype = param_dtype, grad_dtype
         self.struct = s
+
+
+def grad_list(grads: Sequence) -> TensorList:
+    """The list of an OPTIM_ALGO_GRADS plan: gradients of one torch dtype
+    (float32, bfloat16 or float16; int16 is taken for bf16 patterns)."""
+    import torch
+    codes = {torch.float32: OPTIM_F32, torch.bfloat16: OPTIM_BF16, torch.int16: OPTIM_BF16, torch.float16: OPTIM_F16}
+    kinds = {g.dtype for g in grads}
+    if len(kinds) > 1 or not kinds <= set(codes):
+        raise ValueError(f"expected gradients of one type, float32, bfloat16 or float16, got {sorted(map(str, kinds))}")
+    return TensorList([None] * len(grads), grads, weight_decay=[0.0] * len(grads),
+                      numel=[int(g.numel()) for g in grads], grad_dtype=codes[kinds.pop()] if kinds else OPTIM_F32)
 
 
 # --------------------------------------------------------------------------
@@ -315,6 +334,23 @@ def optim_grad_norm(plan, inv_scale_dev, max_norm: float, found_inf_dev, norm_de
                     stream=None) -> None:
     _check(lib().optim_grad_norm(plan, _ptr(inv_scale_dev), float(max_norm), _ptr(found_inf_dev),
                                  _ptr(norm_dev), _ptr(clip_inv_scale_dev), _stream(stream)), "optim_grad_norm")
+
+
+def optim_grad_norms(plan, kind: int, inv_scale_dev, max_norm: float, found_inf_dev, norms_dev, total_dev, coef_dev,
+                     stream=None) -> None:
+    _check(lib().optim_grad_norms(plan, int(kind), _ptr(inv_scale_dev), float(max_norm), _ptr(found_inf_dev),
+                                  _ptr(norms_dev), _ptr(total_dev), _ptr(coef_dev), _stream(stream)),
+           "optim_grad_norms")
+
+
+def optim_clip_coef(norms_dev, count: int, kind: int, inv_scale_dev, max_norm: float, total_dev, coef_dev,
+                    stream=None) -> None:
+    _check(lib().optim_clip_coef(_ptr(norms_dev), int(count), int(kind), _ptr(inv_scale_dev), float(max_norm),
+                                 _ptr(total_dev), _ptr(coef_dev), _stream(stream)), "optim_clip_coef")
+
+
+def optim_clip_grads(plan, coef_dev, found_inf_dev=None, stream=None) -> None:
+    _check(lib().optim_clip_grads(plan, _ptr(coef_dev), _ptr(found_inf_dev), _stream(stream)), "optim_clip_grads")
 
 
 def optim_scaler_update(scale_dev, inv_scale_dev, growth_tracker_dev, found_inf_dev, growth_factor: float,

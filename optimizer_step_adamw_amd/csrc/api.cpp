@@ -1,7 +1,9 @@
 // api.cpp -- C ABI of the fused AdamW-family optimizer step: validation,
 // plan tables (tensor descriptors, unit spans, weight-decay groups,
 // quantization tables), workspace layout and launches.  Declared in
-// include/optim_step.h, which documents each entry point and its sources.
+// include/optim_step.h, which documents each entry point and its sources,
+// and include/optim_grads.h.
+#include "optim_grads.h"
 #include "optim_step.h"
 #include "plan.h"
 
@@ -124,6 +126,10 @@ struct Built {
     std::vector<int32_t> pack_off;
     std::vector<PackMember> pack_td;
     int64_t pack_unit0 = 0;         // first pack unit (packs come last)
+    std::vector<GradTensor> gtensors;  // gradient lists
+    std::vector<GradItem> gitems;
+    std::vector<int32_t> gorder;
+    int64_t gbytes = 0;
     Layout L{};
 };
 
@@ -134,6 +140,25 @@ struct Range {
     const char *what;
 };
 
+// no written buffer may overlap any other buffer of the plan
+int check_overlaps(std::vector<Range> &ranges) {
+    std::sort(ranges.begin(), ranges.end(), [](const Range &a, const Range &b) { return a.lo < b.lo; });
+    uintptr_t end_all = 0, end_w = 0;
+    const Range *cov_all = nullptr, *cov_w = nullptr;
+    for (const Range &r : ranges) {
+        const Range *hit = nullptr;
+        if (r.written && r.lo < end_all) hit = cov_all;
+        else if (!r.written && r.lo < end_w) hit = cov_w;
+        if (hit)
+            return fail(OPTIM_EINVAL, "buffers overlap: tensor " + std::to_string(hit->tensor) + " " +
+                                          hit->what + " and tensor " + std::to_string(r.tensor) + " " +
+                                          r.what);
+        if (r.hi > end_all) { end_all = r.hi; cov_all = &r; }
+        if (r.written && r.hi > end_w) { end_w = r.hi; cov_w = &r; }
+    }
+    return OPTIM_OK;
+}
+
 int check_hp_beta(double b, const char *name) {
     if (!(b >= 0.0 && b < 1.0))
         return fail(OPTIM_EINVAL, std::string("invalid ") + name + " (need 0 <= beta < 1)");
@@ -142,8 +167,67 @@ int check_hp_beta(double b, const char *name) {
 
 bool is_blockwise(int32_t algo) { return algo == OPTIM_ALGO_BLOCKWISE || algo == OPTIM_ALGO_BLOCKWISE_ADEMAMIX; }
 
+// Gradient lists: the item table (see GradItem) and its workspace.
+int build_grads(const optim_tensor_list *list, const optim_plan_opts *opts, Built &B) {
+    const int n = list->n;
+    if (n < 0) return fail(OPTIM_EINVAL, "negative tensor count");
+    if (list->grad_dtype != OPTIM_F32 && list->grad_dtype != OPTIM_BF16 && list->grad_dtype != OPTIM_F16)
+        return fail(OPTIM_EDTYPE, "grad_dtype must be OPTIM_F32, OPTIM_BF16 or OPTIM_F16");
+    if (opts && (opts->grid || opts->tile || opts->state_dtype || opts->state_layout))
+        return fail(OPTIM_EUNSUPPORTED, "gradient lists take no grid, tile, state_dtype or state_layout");
+    if (n > 0 && (!list->numel || !list->grad)) return fail(OPTIM_EINVAL, "numel and grad arrays are required");
+    const size_t gsz = list->grad_dtype == OPTIM_F32 ? 4 : 2;
+    std::vector<Range> ranges;
+    B.gtensors.assign(n, GradTensor{});
+    for (int i = 0; i < n; ++i) {
+        const std::string ti = "tensor " + std::to_string(i) + ": ";
+        const int64_t numel = list->numel[i];
+        if (numel < 0) return fail(OPTIM_EINVAL, ti + "negative numel");
+        if (numel > kMaxNumel) return fail(OPTIM_EINVAL, ti + "numel above 2^48");
+        void *g = const_cast<void *>(list->grad[i]);
+        if (numel > 0 && !g) return fail(OPTIM_EINVAL, ti + "NULL grad");
+        if (!aligned(g, gsz)) return fail(OPTIM_EALIGN, ti + "grad misaligned");
+        GradTensor &T = B.gtensors[i];
+        T.g = g;
+        T.numel = numel;
+        if (numel == 0) continue;
+        ranges.push_back({(uintptr_t)g, (uintptr_t)g + (size_t)numel * gsz, true, i, "grad"});
+        B.gbytes += numel * (int64_t)gsz;
+        if (numel <= kGradSmall) {
+            B.gorder.push_back(i);
+            continue;
+        }
+        const int64_t items = (numel + kGradItem - 1) / kGradItem;
+        if (items + (int64_t)B.gitems.size() >= INT32_MAX) return fail(OPTIM_EUNSUPPORTED, "gradient list too long");
+        T.slot0 = B.npartials;
+        T.nslots = (int32_t)items;
+        if (items > 1) B.npartials += items;
+        for (int64_t k = 0; k < items; ++k)
+            B.gitems.push_back(GradItem{k * kGradItem, i, (int32_t)std::min(kGradItem, numel - k * kGradItem), (int32_t)k, 0});
+    }
+    const int32_t small = (int32_t)B.gorder.size();
+    for (int32_t k = 0; k < small; k += kGradBundle)
+        B.gitems.push_back(GradItem{0, k, 0, 0, std::min(kGradBundle, small - k)});
+    if (const int rc = check_overlaps(ranges)) return rc;
+
+    Layout &L = B.L;
+    size_t off = 0;
+    L.counters = off; off += align256(kCounterBytes);
+    L.group_wd = L.tensors = L.spans = L.codebook = L.blockspan = L.packs = L.pack_off = L.pack_td = L.blockfac = off;
+    L.gtensors = off; off += align256(std::max<size_t>(1, B.gtensors.size()) * sizeof(GradTensor));
+    L.gitems = off; off += align256(std::max<size_t>(1, B.gitems.size()) * sizeof(GradItem));
+    L.gorder = off; off += align256(std::max<size_t>(1, B.gorder.size()) * sizeof(int32_t));
+    L.gcount = off; off += align256(std::max<size_t>(1, B.gtensors.size()) * sizeof(uint32_t));
+    L.gsum = off; off += align256(std::max<size_t>(1, B.gtensors.size()) * sizeof(double));
+    L.partials = off;  // the uploaded image ends here
+    off += align256(std::max<int64_t>(1, B.npartials) * sizeof(double));
+    L.total = off;
+    return OPTIM_OK;
+}
+
 int build(const optim_tensor_list *list, int32_t algo, const optim_plan_opts *opts, Built &B) {
     if (!list) return fail(OPTIM_EINVAL, "tensor list is NULL");
+    if (algo == OPTIM_ALGO_GRADS) return build_grads(list, opts, B);
     if (algo < OPTIM_ALGO_ADAMW || algo > OPTIM_ALGO_LAMB)
         return fail(OPTIM_EINVAL, "unknown algorithm");
     const int n = list->n;
@@ -494,21 +578,7 @@ int build(const optim_tensor_list *list, int32_t algo, const optim_plan_opts *op
         return fail(OPTIM_EUNSUPPORTED, "too many spans");
     B.spans.push_back(SpanDesc{B.nunits, 0, 0, -1, -1});  // sentinel
 
-    // no written buffer may overlap any other buffer of the plan
-    std::sort(ranges.begin(), ranges.end(), [](const Range &a, const Range &b) { return a.lo < b.lo; });
-    uintptr_t end_all = 0, end_w = 0;
-    const Range *cov_all = nullptr, *cov_w = nullptr;
-    for (const Range &r : ranges) {
-        const Range *hit = nullptr;
-        if (r.written && r.lo < end_all) hit = cov_all;
-        else if (!r.written && r.lo < end_w) hit = cov_w;
-        if (hit)
-            return fail(OPTIM_EINVAL, "buffers overlap: tensor " + std::to_string(hit->tensor) + " " +
-                                          hit->what + " and tensor " + std::to_string(r.tensor) + " " +
-                                          r.what);
-        if (r.hi > end_all) { end_all = r.hi; cov_all = &r; }
-        if (r.written && r.hi > end_w) { end_w = r.hi; cov_w = &r; }
-    }
+    if (const int rc = check_overlaps(ranges)) return rc;
 
     Layout &L = B.L;
     size_t off = 0;
@@ -567,6 +637,8 @@ struct optim_plan {
     uint64_t static_gen;
     Trace *trace;  // kernel trace (optim_plan_trace), or NULL
     int64_t pack_unit0;  // first pack unit
+    int32_t ngrads, ngitems;  // gradient lists: tensors, items
+    int64_t gbytes;           // bytes of all gradients
 };
 
 extern "C" {
@@ -678,6 +750,9 @@ int create_on(const Built &B, const optim_tensor_list *list, int32_t algo, const
     std::memcpy(img.data() + B.L.packs, B.packs.data(), B.packs.size() * sizeof(PackDesc));
     std::memcpy(img.data() + B.L.pack_off, B.pack_off.data(), B.pack_off.size() * sizeof(int32_t));
     std::memcpy(img.data() + B.L.pack_td, B.pack_td.data(), B.pack_td.size() * sizeof(PackMember));
+    std::memcpy(img.data() + B.L.gtensors, B.gtensors.data(), B.gtensors.size() * sizeof(GradTensor));
+    std::memcpy(img.data() + B.L.gitems, B.gitems.data(), B.gitems.size() * sizeof(GradItem));
+    std::memcpy(img.data() + B.L.gorder, B.gorder.data(), B.gorder.size() * sizeof(int32_t));
     if (is_blockwise(algo)) {
         Codebook *cb = reinterpret_cast<Codebook *>(img.data() + B.L.codebook);
         if (!build_map(7, cb->m8) || !build_map(8, cb->v8) || !build_map(3, cb->m4) || !build_map(4, cb->v4))
@@ -695,7 +770,7 @@ int create_on(const Built &B, const optim_tensor_list *list, int32_t algo, const
             : !list->master                 ? P_BF16R
             : list->param_dtype == OPTIM_BF16 ? P_MBF16
                                               : P_MF16;
-    P->gk = list->grad_dtype == OPTIM_BF16 ? G_BF16 : G_F32;
+    P->gk = list->grad_dtype == OPTIM_BF16 ? G_BF16 : list->grad_dtype == OPTIM_F16 ? G_F16 : G_F32;
     P->bits = opts ? opts->bits : 0;
     P->block = opts ? opts->block : 0;
     P->grid = opts ? opts->grid : 0;
@@ -715,6 +790,9 @@ int create_on(const Built &B, const optim_tensor_list *list, int32_t algo, const
     P->static_dev = dev;
     P->static_gen = 0;
     P->pack_unit0 = B.pack_unit0;
+    P->ngrads = (int32_t)B.gtensors.size();
+    P->ngitems = (int32_t)B.gitems.size();
+    P->gbytes = B.gbytes;
     *out = P;
     return OPTIM_OK;
 }
@@ -908,6 +986,30 @@ int check_plan(optim_plan *P, int32_t algo, const char *fn) {
     return check_live(P, fn);
 }
 
+GradArgs grad_args(optim_plan *P) {
+    GradArgs a{};
+    a.tensors = reinterpret_cast<const GradTensor *>(P->ws + P->L.gtensors);
+    a.items = reinterpret_cast<const GradItem *>(P->ws + P->L.gitems);
+    a.order = reinterpret_cast<const int32_t *>(P->ws + P->L.gorder);
+    a.count = reinterpret_cast<uint32_t *>(P->ws + P->L.gcount);
+    a.done = reinterpret_cast<uint32_t *>(P->ws + P->L.counters);
+    a.partials = reinterpret_cast<double *>(P->ws + P->L.partials);
+    a.sums = reinterpret_cast<double *>(P->ws + P->L.gsum);
+    a.ntensors = P->ngrads;
+    a.nitems = P->ngitems;
+    a.keep = P->gbytes <= kGradKeepBytes;
+    return a;
+}
+
+int check_norm_args(int32_t kind, const float *inv_scale, double max_norm, const float *total, const float *coef) {
+    if (kind != OPTIM_NORM_L2 && kind != OPTIM_NORM_L1 && kind != OPTIM_NORM_INF)
+        return fail(OPTIM_EINVAL, "unknown norm kind");
+    if (std::isnan(max_norm)) return fail(OPTIM_EINVAL, "max_norm is NaN");
+    if (!aligned(inv_scale, 4) || !aligned(total, 4) || !aligned(coef, 4))
+        return fail(OPTIM_EALIGN, "scalar pointer misaligned");
+    return OPTIM_OK;
+}
+
 // the quantize / dequantize helpers take either blockwise plan
 int check_blockwise_plan(optim_plan *P, const char *fn) {
     if (!P) return fail(OPTIM_EINVAL, std::string(fn) + ": plan is NULL");
@@ -1049,6 +1151,8 @@ int optim_step_8bit_blockwise_ademamix(optim_plan *plan, const optim_ademamix_hp
 int optim_check_finite(optim_plan *plan, float *found_inf_dev, void *stream) {
     if (!plan) return fail(OPTIM_EINVAL, "plan is NULL");
     if (int rc = check_live(plan, "optim_check_finite")) return rc;
+    if (plan->algo == OPTIM_ALGO_GRADS)
+        return fail(OPTIM_EINVAL, "optim_check_finite: a gradient list is checked by optim_grad_norms");
     if (!found_inf_dev || !aligned(found_inf_dev, 4))
         return fail(OPTIM_EINVAL, "found_inf_dev must be an aligned device float");
     if (plan->nunits == 0) return OPTIM_OK;
@@ -1064,6 +1168,8 @@ int optim_grad_norm(optim_plan *plan, const float *inv_scale_dev, double max_nor
                     float *norm_dev, float *clip_inv_scale_dev, void *stream) {
     if (!plan) return fail(OPTIM_EINVAL, "plan is NULL");
     if (int rc = check_live(plan, "optim_grad_norm")) return rc;
+    if (plan->algo == OPTIM_ALGO_GRADS)
+        return fail(OPTIM_EINVAL, "optim_grad_norm: the norms of a gradient list are taken by optim_grad_norms");
     if (!found_inf_dev || !aligned(found_inf_dev, 4))
         return fail(OPTIM_EINVAL, "found_inf_dev must be an aligned device float");
     if (!clip_inv_scale_dev || !aligned(clip_inv_scale_dev, 4))
@@ -1076,6 +1182,38 @@ int optim_grad_norm(optim_plan *plan, const float *inv_scale_dev, double max_nor
     const TraceScope ts(plan);
     HIP_OK(launch_grad_norm(a, plan->gk, inv_scale_dev, max_norm, norm_dev, clip_inv_scale_dev,
                             static_cast<hipStream_t>(stream)));
+    return OPTIM_OK;
+}
+
+int optim_grad_norms(optim_plan *plan, int32_t kind, const float *inv_scale_dev, double max_norm,
+                     float *found_inf_dev, float *norms_dev, float *total_dev, float *coef_dev, void *stream) {
+    if (const int rc = check_plan(plan, OPTIM_ALGO_GRADS, "optim_grad_norms")) return rc;
+    if (const int rc = check_norm_args(kind, inv_scale_dev, max_norm, total_dev, coef_dev)) return rc;
+    if (!total_dev) return fail(OPTIM_EINVAL, "total_dev must be an aligned device float");
+    if (!aligned(found_inf_dev, 4) || !aligned(norms_dev, 4)) return fail(OPTIM_EALIGN, "scalar pointer misaligned");
+    const TraceScope ts(plan);
+    HIP_OK(launch_grad_norms(grad_args(plan), plan->gk, kind, inv_scale_dev, max_norm, found_inf_dev, norms_dev,
+                             total_dev, coef_dev, static_cast<hipStream_t>(stream)));
+    return OPTIM_OK;
+}
+
+int optim_clip_coef(const float *norms_dev, int64_t count, int32_t kind, const float *inv_scale_dev, double max_norm,
+                    float *total_dev, float *coef_dev, void *stream) {
+    if (count < 0) return fail(OPTIM_EINVAL, "negative count");
+    if (count > 0 && !norms_dev) return fail(OPTIM_EINVAL, "NULL norms");
+    if (!aligned(norms_dev, 4)) return fail(OPTIM_EALIGN, "norms misaligned");
+    if (const int rc = check_norm_args(kind, inv_scale_dev, max_norm, total_dev, coef_dev)) return rc;
+    HIP_OK(launch_clip_coef(norms_dev, count, kind, inv_scale_dev, max_norm, total_dev, coef_dev,
+                            static_cast<hipStream_t>(stream)));
+    return OPTIM_OK;
+}
+
+int optim_clip_grads(optim_plan *plan, const float *coef_dev, const float *found_inf_dev, void *stream) {
+    if (const int rc = check_plan(plan, OPTIM_ALGO_GRADS, "optim_clip_grads")) return rc;
+    if (!coef_dev || !aligned(coef_dev, 4)) return fail(OPTIM_EINVAL, "coef_dev must be an aligned device float");
+    if (!aligned(found_inf_dev, 4)) return fail(OPTIM_EALIGN, "scalar pointer misaligned");
+    const TraceScope ts(plan);
+    HIP_OK(launch_clip_grads(grad_args(plan), plan->gk, coef_dev, found_inf_dev, static_cast<hipStream_t>(stream)));
     return OPTIM_OK;
 }
 

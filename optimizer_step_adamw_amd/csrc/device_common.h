@@ -475,17 +475,30 @@ __device__ __forceinline__ uint32_t arrive(uint32_t *c) {
 
 // Called by thread 0 of every workgroup; true in the last one to arrive
 // (the counters are rearmed by then).
-__device__ __forceinline__ bool last_arrival(const StepArgs &a) {
+__device__ __forceinline__ bool last_arrival(uint32_t *done) {
     const uint32_t G = gridDim.x, b = blockIdx.x;
     const uint32_t nsub = G < (uint32_t)kSubCounters ? G : (uint32_t)kSubCounters;
     const uint32_t j = b % nsub;
     const uint32_t members = G / nsub + (j < G % nsub ? 1u : 0u);
-    uint32_t *sub = a.done + (1 + j) * kCounterStride;
+    uint32_t *sub = done + (1 + j) * kCounterStride;
     if (arrive(sub) != members - 1) return false;
     __hip_atomic_store(sub, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if (arrive(a.done) != nsub - 1) return false;
-    __hip_atomic_store(a.done, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (arrive(done) != nsub - 1) return false;
+    __hip_atomic_store(done, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     return true;
+}
+__device__ __forceinline__ bool last_arrival(const StepArgs &a) { return last_arrival(a.done); }
+
+// A value that another workgroup of the same launch reads: stored and loaded
+// at device scope, past the XCD's own L2.  The writer waits here for its
+// store, so an arrival (arrive()) of its workgroup after that means it is
+// there; the reader loads after it has seen the arrival.
+__device__ __forceinline__ void publish(double *p, double x) {
+    __hip_atomic_store(p, x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+__device__ __forceinline__ double published(const double *p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 __device__ __forceinline__ void publish_step(const StepArgs &a, const Scalars &S) {

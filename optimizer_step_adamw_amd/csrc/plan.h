@@ -60,7 +60,7 @@ constexpr int64_t kMaxNumel = int64_t(1) << 48;  // per tensor (byte sizes stay 
 
 // fp32; bf16 + int16 remainder; fp32 master + bf16 or fp16 model copy
 enum ParamKind { P_F32 = 0, P_BF16R = 1, P_MBF16 = 2, P_MF16 = 3 };
-enum GradKind { G_F32 = 0, G_BF16 = 1 };
+enum GradKind { G_F32 = 0, G_BF16 = 1, G_F16 = 2 };  // G_F16: gradient lists only
 // 16-bit scaled moments (same codes as the public state_dtype values)
 enum StateKind { S_BF16 = 1, S_F16 = 2 };
 
@@ -177,11 +177,40 @@ constexpr size_t kCounterBytes = (1 + kSubCounters) * kCounterStride * sizeof(ui
 constexpr int kAmaxSlots = 16;
 constexpr size_t kAmaxBytesPerBlock = 2 * kAmaxSlots * kCounterStride * sizeof(uint32_t);
 
+// Gradient lists (OPTIM_ALGO_GRADS): one workgroup per item.  An item is
+// either up to kGradItem elements of one tensor, or a bundle of whole small
+// tensors, which the workgroup's wavefronts take one each at a time.
+constexpr int64_t kGradItem = 32768;
+constexpr int64_t kGradSmall = 4096;   // tensors of at most this many elements are bundled
+constexpr int32_t kGradBundle = 16;    // tensors per bundle at most
+// lists of at most this many bytes are left in the 256 MB Infinity Cache by
+// the norms' read, for the clip that follows
+constexpr int64_t kGradKeepBytes = int64_t(256) << 20;
+struct GradTensor {       // 32 bytes
+    void *g;
+    int64_t numel;
+    int64_t slot0;        // first partial sum (tensors of more than one item)
+    int32_t nslots;       // items of the tensor (0: bundled or empty)
+    int32_t pad_;
+};
+static_assert(sizeof(GradTensor) == 32, "GradTensor layout");
+struct GradItem {         // 24 bytes
+    int64_t start;        // first element (single tensor)
+    int32_t tensor;       // its tensor; bundle: its first place in `order`
+    int32_t len;          // elements; bundle: 0
+    int32_t slot;         // which of the tensor's items this is
+    int32_t count;        // bundle: tensors
+};
+static_assert(sizeof(GradItem) == 24, "GradItem layout");
+
 // Workspace layout (byte offsets from the workspace base, 256-aligned).
 // `counters` holds the arrival counters of the step kernels' commit.
 struct Layout {
     size_t counters, group_wd, tensors, spans, codebook, partials, blockfac,
         blockspan, packs, pack_off, pack_td, total;
+    // gradient lists: tensors, items, the bundled tensors' indexes, arrival
+    // counters and sums of the tensors
+    size_t gtensors, gitems, gorder, gcount, gsum;
 };
 
 // Quantization maps.  A normalised magnitude a in [0, 1] maps to the largest
@@ -303,6 +332,24 @@ int64_t finite_pass_grid(int64_t nunits, int64_t tile, int32_t grid_request);
 int64_t norm_partials(int64_t nunits, int64_t tile, int32_t grid_request);
 hipError_t launch_grad_norm(const StepArgs &a, int gk, const float *inv_scale, double max_norm,
                             float *norm_out, float *clip_out, hipStream_t s);
+// Gradient lists (kernels_grads.hip).  kind: OPTIM_NORM_*.
+struct GradArgs {
+    const GradTensor *tensors;
+    const GradItem *items;
+    const int32_t *order;  // indexes of the bundled tensors
+    uint32_t *count;       // per tensor: items that have arrived, 0 between calls
+    uint32_t *done;        // arrival counters of the launch, 0 between calls
+    double *partials;      // one per item of a tensor of several
+    double *sums;          // one per tensor
+    int32_t ntensors;
+    int32_t nitems;
+    int32_t keep;          // the list is read again soon: leave it in the cache
+};
+hipError_t launch_grad_norms(const GradArgs &a, int gk, int kind, const float *inv_scale, double max_norm,
+                             float *found_inf, float *norms, float *total, float *coef, hipStream_t s);
+hipError_t launch_clip_grads(const GradArgs &a, int gk, const float *coef, const float *found_inf, hipStream_t s);
+hipError_t launch_clip_coef(const float *norms, int64_t count, int kind, const float *inv_scale, double max_norm,
+                            float *total, float *coef, hipStream_t s);
 hipError_t launch_scaler_update(float *scale, float *inv_scale, int32_t *tracker, const float *found_inf,
                                 double growth, double backoff, int32_t interval, hipStream_t s);
 hipError_t launch_quantize(const Codebook *cb, int bits, int block, int is_signed, const float *x,
