@@ -95,6 +95,8 @@ enum { OPTIM_SCHED_NONE = 0, OPTIM_SCHED_COSINE = 1 };
  *               model param), AdamW and AdEMAMix only: the step updates the
  *               master and rewrites param as the master rounded to nearest
  *               even.  remainder must be NULL then.  NULL otherwise.
+ *  rows, cols   OPTIM_ALGO_MUON only (optim_muon.h): sides of a tensor's
+ *               matrices; NULL otherwise
  *  weight_decay per-tensor decoupled decay (>= 0)
  *  mini_kind    Adam-mini only: OPTIM_MINI_*
  *  head_numel   Adam-mini only: block length for HEAD (must divide numel);
@@ -124,6 +126,8 @@ typedef struct optim_tensor_list {
     float *const *master;
     float *const *scale_m;
     float *const *scale_v;
+    const int64_t *rows;
+    const int64_t *cols;
 } optim_tensor_list;
 
 /* Plan options (NULL = all defaults).
@@ -143,7 +147,8 @@ typedef struct optim_tensor_list {
  *  state_dtype AdamW only: OPTIM_F32 (0, default) fp32 moments; OPTIM_F16
  *              or OPTIM_BF16 16-bit moments with a per-tensor scale
  *              ([TE] review: state scaling), see optim_step_adamw
- *  segment_bytes  Adam-mini only: the step runs its block-sum, finalize
+ *  segment_bytes  Adam-mini (Muon: see optim_muon.h): the step
+ *              runs its block-sum, finalize
  *              and update kernels once per segment, a run of consecutive
  *              whole tensors with shared v holding at most this many
  *              gradient bytes (a larger tensor forms a segment alone), or a

@@ -3,8 +3,8 @@ for AMD Instinct MI355X (gfx950).
 
 Argument marshalling only: torch tensors are turned into device pointers and a
 HIP stream handle; every step of the computation runs in the library's HIP
-kernels.  Functions keep the C names of ``include/optim_step.h`` and
-``include/optim_grads.h``.  If the
+kernels.  Functions keep the C names of ``include/optim_step.h``,
+``include/optim_grads.h`` and ``include/optim_muon.h``.  If the
 library has not been built, importing the binding works but every call raises
 ``RuntimeError`` -- there is no fallback path.
 """
@@ -23,6 +23,7 @@ OPTIM_LAYOUT_SEPARATE, OPTIM_LAYOUT_INTERLEAVED = 0, 1
 (OPTIM_ALGO_ADAMW, OPTIM_ALGO_ADEMAMIX, OPTIM_ALGO_ADAM_MINI, OPTIM_ALGO_BLOCKWISE,
  OPTIM_ALGO_BLOCKWISE_ADEMAMIX, OPTIM_ALGO_LION, OPTIM_ALGO_LAMB, OPTIM_ALGO_MUON, OPTIM_ALGO_GRADS) = range(9)
 OPTIM_NORM_L2, OPTIM_NORM_L1, OPTIM_NORM_INF = range(3)
+OPTIM_MUON_SCALE_NONE, OPTIM_MUON_SCALE_ASPECT, OPTIM_MUON_SCALE_RMS = range(3)
 OPTIM_MINI_FULL_V, OPTIM_MINI_HEAD, OPTIM_MINI_SCALAR = range(3)
 OPTIM_SCHED_NONE, OPTIM_SCHED_COSINE = 0, 1
 
@@ -37,6 +38,8 @@ EXPORTED = (
 )
 # entry points of include/optim_grads.h
 EXPORTED_GRADS = ("optim_grad_norms", "optim_clip_coef", "optim_clip_grads")
+# entry points of include/optim_muon.h
+EXPORTED_MUON = ("optim_step_muon",)
 # bytes of the library's static per-device workspace (optim_plan_create_static)
 OPTIM_STATIC_WORKSPACE_BYTES = 16 << 20
 
@@ -63,6 +66,7 @@ class optim_tensor_list(ctypes.Structure):
         ("param_dtype", ctypes.c_int32),
         ("grad_dtype", ctypes.c_int32),
         ("qm2", _PP), ("absmax_m2", _PP), ("master", _PP), ("scale_m", _PP), ("scale_v", _PP),
+        ("rows", ctypes.POINTER(ctypes.c_int64)), ("cols", ctypes.POINTER(ctypes.c_int64)),
     ]
 
 
@@ -87,6 +91,17 @@ class optim_lion_hp(ctypes.Structure):
 class optim_ademamix_hp(ctypes.Structure):
     _fields_ = [("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("beta3", ctypes.c_double),
                 ("alpha", ctypes.c_double), ("eps", ctypes.c_double)]
+
+
+class optim_muon_hp(ctypes.Structure):
+    """Momentum and the quintic of Jordan et al. (2024) by default."""
+    _fields_ = [("momentum", ctypes.c_double), ("eps", ctypes.c_double), ("a", ctypes.c_double), ("b", ctypes.c_double),
+                ("c", ctypes.c_double), ("steps", ctypes.c_int32), ("nesterov", ctypes.c_int32),
+                ("scale_kind", ctypes.c_int32)]
+
+    def __init__(self, momentum=0.95, eps=1e-7, a=3.4445, b=-4.7750, c=2.0315, steps=5, nesterov=1,
+                 scale_kind=OPTIM_MUON_SCALE_RMS):
+        super().__init__(momentum, eps, a, b, c, steps, nesterov, scale_kind)
 
 
 _lib = None
@@ -131,6 +146,7 @@ def lib() -> ctypes.CDLL:
                                                     _P, _P, _P], i32),
             "optim_step_lion": ([_P, ctypes.POINTER(optim_lion_hp), _P, _P, _P, _P, _P], i32),
             "optim_step_lamb": ([_P, ctypes.POINTER(optim_adamw_hp), _P, _P, _P, _P, _P], i32),
+            "optim_step_muon": ([_P, ctypes.POINTER(optim_muon_hp), _P, _P, _P, _P, _P], i32),
             "optim_grad_norms": ([_P, i32, _P, f64, _P, _P, _P, _P, _P], i32),
             "optim_clip_coef": ([_P, i64, i32, _P, f64, _P, _P, _P], i32),
             "optim_clip_grads": ([_P, _P, _P, _P], i32),
@@ -179,7 +195,7 @@ class TensorList:
     def __init__(self, params: Sequence, grads: Sequence, *, m=None, v=None, m2=None,
                  remainders=None, qm=None, qv=None, absmax_m=None, absmax_v=None,
                  qm2=None, absmax_m2=None, master=None, scale_m=None, scale_v=None,
-                 weight_decay: Sequence[float], mini_kind=None, head_numel=None,
+                 weight_decay: Sequence[float], mini_kind=None, head_numel=None, rows=None, cols=None,
                  param_dtype: int = OPTIM_F32, grad_dtype: int = OPTIM_F32,
                  numel: Optional[Sequence[int]] = None):
         n = len(params)
@@ -210,6 +226,12 @@ class TensorList:
             self._hn = (ctypes.c_int64 * max(n, 1))(*(head_numel or [0] * n))
             s.mini_kind = ctypes.cast(self._kind, ctypes.POINTER(ctypes.c_int32))
             s.head_numel = ctypes.cast(self._hn, ctypes.POINTER(ctypes.c_int64))
+        if rows is not None:
+            self._rows = (ctypes.c_int64 * max(n, 1))(*[int(r) for r in rows])
+            s.rows = ctypes.cast(self._rows, ctypes.POINTER(ctypes.c_int64))
+        if cols is not None:
+            self._cols = (ctypes.c_int64 * max(n, 1))(*[int(c) for c in cols])
+            s.cols = ctypes.cast(self._cols, ctypes.POINTER(ctypes.c_int64))
         s.param_dtype, s.grad_dtype = param_dtype, grad_dtype
         self.struct = s
 
@@ -316,6 +338,11 @@ def optim_step_lamb(plan, hp: optim_adamw_hp, lr_dev, inv_scale_dev, found_inf_d
                     stream=None) -> None:
     _check(lib().optim_step_lamb(plan, ctypes.byref(hp), _ptr(lr_dev), _ptr(inv_scale_dev), _ptr(found_inf_dev),
                                  _ptr(step_dev), _stream(stream)), "optim_step_lamb")
+
+
+def optim_step_muon(plan, hp: optim_muon_hp, lr_dev, inv_scale_dev, found_inf_dev, step_dev, stream=None) -> None:
+    _check(lib().optim_step_muon(plan, ctypes.byref(hp), _ptr(lr_dev), _ptr(inv_scale_dev), _ptr(found_inf_dev),
+                                 _ptr(step_dev), _stream(stream)), "optim_step_muon")
 
 
 def optim_step_8bit_blockwise_ademamix(plan, hp: optim_ademamix_hp, bits: int, block: int, lr_dev,

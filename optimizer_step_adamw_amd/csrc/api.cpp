@@ -2,8 +2,9 @@
 // plan tables (tensor descriptors, unit spans, weight-decay groups,
 // quantization tables), workspace layout and launches.  Declared in
 // include/optim_step.h, which documents each entry point and its sources,
-// and include/optim_grads.h.
+// include/optim_grads.h and include/optim_muon.h.
 #include "optim_grads.h"
+#include "optim_muon.h"
 #include "optim_step.h"
 #include "plan.h"
 
@@ -130,6 +131,10 @@ struct Built {
     std::vector<GradItem> gitems;
     std::vector<int32_t> gorder;
     int64_t gbytes = 0;
+    std::vector<MuonMat> mats;      // Muon
+    std::vector<MuonTile> sym, full;
+    std::vector<MuonRun> runs;
+    int64_t muon_bytes = 0;         // of the region the runs share
     Layout L{};
 };
 
@@ -166,6 +171,64 @@ int check_hp_beta(double b, const char *name) {
 }
 
 bool is_blockwise(int32_t algo) { return algo == OPTIM_ALGO_BLOCKWISE || algo == OPTIM_ALGO_BLOCKWISE_ADEMAMIX; }
+
+int64_t pad_tile(int64_t n) { return (n + kMuonTile - 1) / kMuonTile * kMuonTile; }
+
+// Muon: the matrices of tensor i, their arrays and tiles.  A run takes
+// matrices until their arrays pass `cap` bytes.
+int add_matrices(const std::string &ti, int i, int64_t numel, int64_t rows, int64_t cols, int64_t cap, Built &B) {
+    if (rows < 1 || cols < 1 || rows > kMuonMaxSide || cols > kMuonMaxSide)
+        return fail(OPTIM_EINVAL, ti + "rows and cols must be in [1, 2^20]");
+    if (numel % (rows * cols) != 0) return fail(OPTIM_EINVAL, ti + "numel must be a multiple of rows * cols");
+    const int64_t count = numel / (rows * cols);
+    const int64_t rp = pad_tile(rows), ld = pad_tile(cols), sp = std::min(rp, ld);
+    const int64_t bytes = 2 * (rp * ld * 4) + 2 * (sp * sp * 4);
+    const int64_t nt = sp / kMuonTile;
+    const int64_t tiles = nt * (nt + 1) / 2 + (rp / kMuonTile) * (ld / kMuonTile);
+    if (count > INT32_MAX / 4 || (int64_t)B.mats.size() + count > INT32_MAX / 4 ||
+        tiles > (((int64_t)1 << 26) - (int64_t)(B.sym.size() + B.full.size())) / count)
+        return fail(OPTIM_EUNSUPPORTED, ti + "too many matrices or tiles");
+    for (int64_t k = 0; k < count; ++k) {
+        int64_t used = B.mats.empty() ? 0 : B.mats.back().b + (int64_t)B.mats.back().sp * B.mats.back().sp * 4;
+        if (B.runs.empty() || used + bytes > cap) {
+            const int32_t m = (int32_t)B.mats.size();
+            B.runs.push_back(MuonRun{m, m, 0, (int64_t)B.sym.size(), 0, (int64_t)B.full.size(), 0});
+            used = 0;
+        }
+        MuonRun &R = B.runs.back();
+        MuonMat M{};
+        M.elem0 = k * rows * cols;
+        M.x[0] = used;
+        M.x[1] = M.x[0] + rp * ld * 4;
+        M.a = M.x[1] + rp * ld * 4;
+        M.b = M.a + sp * sp * 4;
+        M.unit0 = R.units;
+        M.tensor = i;
+        M.rows = (int32_t)rows;
+        M.cols = (int32_t)cols;
+        M.ld = (int32_t)ld;
+        M.rp = (int32_t)rp;
+        M.sp = (int32_t)sp;
+        M.tall = rows > cols;
+        const int32_t m = (int32_t)B.mats.size();
+        B.mats.push_back(M);
+        for (int64_t a = 0; a < nt; ++a)
+            for (int64_t b = a; b < nt; ++b) B.sym.push_back(MuonTile{m, (uint16_t)a, (uint16_t)b});
+        for (int64_t a = 0; a < rp / kMuonTile; ++a)
+            for (int64_t b = 0; b < ld / kMuonTile; ++b) B.full.push_back(MuonTile{m, (uint16_t)a, (uint16_t)b});
+        R.mat1 = m + 1;
+        R.units += rp * ld / kMuonUnit;
+        R.nsym = (int64_t)B.sym.size() - R.sym0;
+        R.nfull = (int64_t)B.full.size() - R.full0;
+        B.muon_bytes = std::max(B.muon_bytes, used + bytes);
+        // a span per matrix: its units' sums of squares give its norm
+        B.blockspan.push_back((int32_t)B.spans.size());
+        B.spans.push_back(SpanDesc{B.nunits, M.elem0, rows * cols, i, B.nblocks});
+        B.nunits += (rows * cols + B.tile - 1) / B.tile;
+        ++B.nblocks;
+    }
+    return OPTIM_OK;
+}
 
 // Gradient lists: the item table (see GradItem) and its workspace.
 int build_grads(const optim_tensor_list *list, const optim_plan_opts *opts, Built &B) {
@@ -228,8 +291,9 @@ int build_grads(const optim_tensor_list *list, const optim_plan_opts *opts, Buil
 int build(const optim_tensor_list *list, int32_t algo, const optim_plan_opts *opts, Built &B) {
     if (!list) return fail(OPTIM_EINVAL, "tensor list is NULL");
     if (algo == OPTIM_ALGO_GRADS) return build_grads(list, opts, B);
-    if (algo < OPTIM_ALGO_ADAMW || algo > OPTIM_ALGO_LAMB)
+    if (algo < OPTIM_ALGO_ADAMW || algo > OPTIM_ALGO_MUON)
         return fail(OPTIM_EINVAL, "unknown algorithm");
+    const bool muon = algo == OPTIM_ALGO_MUON;
     const int n = list->n;
     if (n < 0) return fail(OPTIM_EINVAL, "negative tensor count");
     const int32_t pdt = list->param_dtype;
@@ -240,8 +304,8 @@ int build(const optim_tensor_list *list, int32_t algo, const optim_plan_opts *op
     const bool masterw = list->master != nullptr;
     if (masterw && pdt == OPTIM_F32) return fail(OPTIM_EINVAL, "master weights need a BF16 or F16 model param");
     if (pdt == OPTIM_F16 && !masterw) return fail(OPTIM_EUNSUPPORTED, "F16 params need fp32 master weights");
-    if (masterw && algo != OPTIM_ALGO_ADAMW && algo != OPTIM_ALGO_ADEMAMIX)
-        return fail(OPTIM_EUNSUPPORTED, "master weights are supported for AdamW and AdEMAMix");
+    if (masterw && algo != OPTIM_ALGO_ADAMW && algo != OPTIM_ALGO_ADEMAMIX && !muon)
+        return fail(OPTIM_EUNSUPPORTED, "master weights are supported for AdamW, AdEMAMix and Muon");
     const bool bf16p = pdt == OPTIM_BF16 && !masterw;  // bf16 + remainder
     if (pdt != OPTIM_F32 && is_blockwise(algo))
         return fail(OPTIM_EUNSUPPORTED, "blockwise states take fp32 params only");
@@ -272,10 +336,13 @@ int build(const optim_tensor_list *list, int32_t algo, const optim_plan_opts *op
     const bool mom_il = layout == OPTIM_LAYOUT_INTERLEAVED && adam_like;
     B.interleaved = il || mom_il;
     if (opts && opts->grid < 0) return fail(OPTIM_EINVAL, "negative grid");
+    if (opts && opts->grid && muon) return fail(OPTIM_EUNSUPPORTED, "Muon takes no persistent grid");
     B.grid = opts ? opts->grid : 0;
     if (opts && opts->tile < 0) return fail(OPTIM_EINVAL, "negative tile");
     if (opts && opts->segment_bytes < 0) return fail(OPTIM_EINVAL, "negative segment_bytes");
-    const int64_t seg_cap = (opts && opts->segment_bytes > 0) ? opts->segment_bytes : kMiniSegmentBytes;
+    const int64_t seg_cap = (opts && opts->segment_bytes > 0) ? opts->segment_bytes
+                            : muon                            ? kMuonRunBytes
+                                                              : kMiniSegmentBytes;
     bool seg_shared = false;
     int64_t seg_gbytes = 0;
     const int32_t sdt = opts ? opts->state_dtype : OPTIM_F32;
@@ -315,10 +382,12 @@ int build(const optim_tensor_list *list, int32_t algo, const optim_plan_opts *op
     B.tile = tile;
     if (n > 0 && (!list->numel || !list->param || !list->grad || !list->weight_decay))
         return fail(OPTIM_EINVAL, "numel, param, grad and weight_decay arrays are required");
-    const bool need_mv = !is_blockwise(algo) && algo != OPTIM_ALGO_LION;
+    const bool need_mv = !is_blockwise(algo) && algo != OPTIM_ALGO_LION && !muon;
     if (n > 0 && need_mv && (!list->m || (!mom_il && !list->v)))
         return fail(OPTIM_EINVAL, mom_il ? "the m array is required" : "m and v arrays are required");
     if (n > 0 && algo == OPTIM_ALGO_LION && !list->m) return fail(OPTIM_EINVAL, "Lion needs the m array");
+    if (n > 0 && muon && (!list->m || !list->rows || !list->cols))
+        return fail(OPTIM_EINVAL, "Muon needs the m, rows and cols arrays");
     if (n > 0 && algo == OPTIM_ALGO_ADEMAMIX && !mom_il && !list->m2)
         return fail(OPTIM_EINVAL, "AdEMAMix needs the m2 array");
     if (n > 0 && is_blockwise(algo) && (!list->qm || (!il && !list->qv) || !list->absmax_m || (!il && !list->absmax_v)))
@@ -471,7 +540,7 @@ int build(const optim_tensor_list *list, int32_t algo, const optim_plan_opts *op
                 add(T.scale_v, 4, true, "scale_v");
             }
         }
-        if (algo == OPTIM_ALGO_LION) {
+        if (algo == OPTIM_ALGO_LION || muon) {
             T.m = static_cast<float *>(list->m[i]);
             if (numel > 0 && !T.m) return fail(OPTIM_EINVAL, ti + "NULL m");
             if (!aligned(T.m, 4)) return fail(OPTIM_EALIGN, ti + "m misaligned");
@@ -535,6 +604,8 @@ int build(const optim_tensor_list *list, int32_t algo, const optim_plan_opts *op
                 if (B.nblocks == INT32_MAX) return fail(OPTIM_EUNSUPPORTED, "too many blocks");
                 ++B.nblocks;
             }
+        } else if (muon) {
+            if (const int rc = add_matrices(ti, i, numel, list->rows[i], list->cols[i], seg_cap, B)) return rc;
         } else if (algo == OPTIM_ALGO_LAMB || states16) {
             // one block per tensor: its trust ratio, or its state scales
             B.blockspan.push_back((int32_t)B.spans.size());
@@ -591,12 +662,15 @@ int build(const optim_tensor_list *list, int32_t algo, const optim_plan_opts *op
     L.packs = off; off += align256(B.packs.size() * sizeof(PackDesc));
     L.pack_off = off; off += align256(B.pack_off.size() * sizeof(int32_t));
     L.pack_td = off; off += align256(B.pack_td.size() * sizeof(PackMember));
+    L.mats = off; off += align256(B.mats.size() * sizeof(MuonMat));
+    L.sym = off; off += align256(B.sym.size() * sizeof(MuonTile));
+    L.full = off; off += align256(B.full.size() * sizeof(MuonTile));
     // partial sums: Adam-mini's block sums (one per unit) and the gradient
     // norm pass (one per workgroup) share the region; they never overlap in
     // stream order
     L.partials = off;
     // (LAMB: two per unit, sums of p^2 and u^2)
-    B.npartials = std::max<int64_t>(algo == OPTIM_ALGO_ADAM_MINI ? B.nunits
+    B.npartials = std::max<int64_t>(algo == OPTIM_ALGO_ADAM_MINI || muon ? B.nunits
                                     : algo == OPTIM_ALGO_LAMB    ? 2 * B.nunits
                                                                  : 0,
                                     norm_partials(B.nunits, B.tile, B.grid));
@@ -606,6 +680,7 @@ int build(const optim_tensor_list *list, int32_t algo, const optim_plan_opts *op
     L.blockfac = off;
     off += align256(B.states16 ? std::max<int32_t>(1, B.nblocks) * kAmaxBytesPerBlock
                                : std::max<int32_t>(1, 2 * B.nblocks) * sizeof(float));
+    L.muon = off; off += align256((size_t)B.muon_bytes);
     L.total = off;
     return OPTIM_OK;
 }
@@ -626,6 +701,7 @@ struct optim_plan {
     char *ws;
     Layout L;
     std::vector<MiniSegment> segs;  // Adam-mini launch segments
+    std::vector<MuonRun> runs;      // Muon: runs of launches
     int32_t interleaved;            // blockwise: interleaved state layout
     int32_t sched;
     double lr_max, lr_min;
@@ -750,6 +826,9 @@ int create_on(const Built &B, const optim_tensor_list *list, int32_t algo, const
     std::memcpy(img.data() + B.L.packs, B.packs.data(), B.packs.size() * sizeof(PackDesc));
     std::memcpy(img.data() + B.L.pack_off, B.pack_off.data(), B.pack_off.size() * sizeof(int32_t));
     std::memcpy(img.data() + B.L.pack_td, B.pack_td.data(), B.pack_td.size() * sizeof(PackMember));
+    std::memcpy(img.data() + B.L.mats, B.mats.data(), B.mats.size() * sizeof(MuonMat));
+    std::memcpy(img.data() + B.L.sym, B.sym.data(), B.sym.size() * sizeof(MuonTile));
+    std::memcpy(img.data() + B.L.full, B.full.data(), B.full.size() * sizeof(MuonTile));
     std::memcpy(img.data() + B.L.gtensors, B.gtensors.data(), B.gtensors.size() * sizeof(GradTensor));
     std::memcpy(img.data() + B.L.gitems, B.gitems.data(), B.gitems.size() * sizeof(GradItem));
     std::memcpy(img.data() + B.L.gorder, B.gorder.data(), B.gorder.size() * sizeof(int32_t));
@@ -785,6 +864,7 @@ int create_on(const Built &B, const optim_tensor_list *list, int32_t algo, const
     P->ws = static_cast<char *>(workspace);
     P->L = B.L;
     P->segs = B.segs;
+    P->runs = B.runs;
     P->interleaved = B.interleaved ? 1 : 0;
     P->sched = OPTIM_SCHED_NONE;
     P->static_dev = dev;
@@ -986,6 +1066,51 @@ int check_plan(optim_plan *P, int32_t algo, const char *fn) {
     return check_live(P, fn);
 }
 
+// The largest |x| over |s| <= R of s (a + b s^2 + c s^4), and of b s^2 +
+// c s^4: each is monotone between its critical points, which are roots of
+// quadratics in s^2.
+void quintic_bounds(double a, double b, double c, double R, double &x, double &y) {
+    double at[4] = {R * R, 0.0, 0.0, 0.0};  // values of s^2
+    int n = 1;
+    auto add = [&](double t) {
+        if (t > 0.0 && t < R * R) at[n++] = t;
+    };
+    if (c != 0.0) {
+        add(-b / (2.0 * c));
+        const double d = 9.0 * b * b - 20.0 * a * c;
+        if (d >= 0.0) {
+            add((-3.0 * b + std::sqrt(d)) / (10.0 * c));
+            add((-3.0 * b - std::sqrt(d)) / (10.0 * c));
+        }
+    } else if (b != 0.0) {
+        add(-a / (3.0 * b));
+    }
+    x = y = 0.0;
+    for (int i = 0; i < n; ++i) {
+        x = std::max(x, std::sqrt(at[i]) * std::fabs(a + at[i] * (b + c * at[i])));
+        y = std::max(y, at[i] * std::fabs(b + c * at[i]));
+    }
+}
+
+int check_muon_hp(const optim_muon_hp *hp) {
+    if (!hp) return fail(OPTIM_EINVAL, "hyperparameters are NULL");
+    if (const int rc = check_hp_beta(hp->momentum, "momentum")) return rc;
+    if (!std::isfinite(hp->a) || !std::isfinite(hp->b) || !std::isfinite(hp->c))
+        return fail(OPTIM_EINVAL, "invalid polynomial (need finite a, b, c)");
+    if (hp->steps < 1 || hp->steps > 16) return fail(OPTIM_EINVAL, "steps must be in [1, 16]");
+    if (hp->scale_kind < OPTIM_MUON_SCALE_NONE || hp->scale_kind > OPTIM_MUON_SCALE_RMS)
+        return fail(OPTIM_EINVAL, "unknown scale_kind");
+    double R = 1.0;
+    for (int i = 0; i < hp->steps; ++i) {
+        double x, y;
+        quintic_bounds(hp->a, hp->b, hp->c, R, x, y);
+        if (!(x <= 15.0) || !(y <= 15.0) || !(R * R <= 15.0))
+            return fail(OPTIM_EINVAL, "the polynomial leaves the range of its 16-bit parts (|X|, |A|, |B| <= 15)");
+        R = std::max(1.0, x);
+    }
+    return OPTIM_OK;
+}
+
 GradArgs grad_args(optim_plan *P) {
     GradArgs a{};
     a.tensors = reinterpret_cast<const GradTensor *>(P->ws + P->L.gtensors);
@@ -1111,6 +1236,29 @@ int optim_step_lamb(optim_plan *plan, const optim_adamw_hp *hp, float *lr_dev, c
     if (rc) return rc;
     const TraceScope ts(plan);
     HIP_OK(launch_lamb(a, plan->pk, plan->gk, static_cast<hipStream_t>(stream)));
+    return OPTIM_OK;
+}
+
+int optim_step_muon(optim_plan *plan, const optim_muon_hp *hp, float *lr_dev, const float *inv_scale_dev,
+                    const float *found_inf_dev, int32_t *step_dev, void *stream) {
+    int rc = check_plan(plan, OPTIM_ALGO_MUON, "optim_step_muon");
+    if (!rc) rc = check_muon_hp(hp);
+    if (rc) return rc;
+    StepArgs a;
+    rc = step_inputs(plan, hp->momentum, 0.0, 0.0, 0.0, hp->eps, lr_dev, inv_scale_dev, found_inf_dev, step_dev, a);
+    if (rc) return rc;
+    MuonArgs ma{};
+    ma.mats = reinterpret_cast<const MuonMat *>(plan->ws + plan->L.mats);
+    ma.sym = reinterpret_cast<const MuonTile *>(plan->ws + plan->L.sym);
+    ma.full = reinterpret_cast<const MuonTile *>(plan->ws + plan->L.full);
+    ma.ws = plan->ws + plan->L.muon;
+    ma.qa = (float)hp->a;
+    ma.qb = (float)hp->b;
+    ma.qc = (float)hp->c;
+    ma.scale_kind = hp->scale_kind;
+    const TraceScope ts(plan);
+    HIP_OK(launch_muon(a, ma, plan->pk, plan->gk, hp->steps, hp->nesterov != 0, plan->runs.data(),
+                       (int32_t)plan->runs.size(), static_cast<hipStream_t>(stream)));
     return OPTIM_OK;
 }
 

@@ -203,6 +203,37 @@ struct GradItem {         // 24 bytes
 };
 static_assert(sizeof(GradItem) == 24, "GradItem layout");
 
+// Muon: a matrix of the list with its arrays in the workspace (byte offsets
+// from the region that the runs share).  X is held padded to rp x ld, A and B
+// to sp x sp, sides rounded up to whole product tiles.
+constexpr int kMuonTile = 128;
+constexpr int64_t kMuonUnit = 4096;  // elements of padded X per workgroup of the splitting pass
+constexpr int64_t kMuonMaxSide = int64_t(1) << 20;
+constexpr int64_t kMuonRunBytes = int64_t(4) << 30;  // workspace of one run of launches
+struct MuonMat {          // 80 bytes
+    int64_t elem0;        // its first element in the tensor
+    int64_t x[2], a, b;   // X (read and written in turn), A, B
+    int64_t unit0;        // first unit of the splitting pass, within its run
+    int32_t tensor;
+    int32_t rows, cols;
+    int32_t ld, rp;       // padded columns and rows of X
+    int32_t sp;           // padded shorter side
+    int32_t tall;         // rows > cols
+    int32_t pad_;
+};
+static_assert(sizeof(MuonMat) == 80, "MuonMat layout");
+struct MuonTile {         // 8 bytes
+    int32_t mat;
+    uint16_t i, j;        // tile row and column
+};
+static_assert(sizeof(MuonTile) == 8, "MuonTile layout");
+struct MuonRun {          // matrices [mat0, mat1) that share a run of launches
+    int32_t mat0, mat1;
+    int64_t units;        // of the splitting pass
+    int64_t sym0, nsym;   // tiles of the symmetric products
+    int64_t full0, nfull; // tiles of X
+};
+
 // Workspace layout (byte offsets from the workspace base, 256-aligned).
 // `counters` holds the arrival counters of the step kernels' commit.
 struct Layout {
@@ -211,6 +242,9 @@ struct Layout {
     // gradient lists: tensors, items, the bundled tensors' indexes, arrival
     // counters and sums of the tensors
     size_t gtensors, gitems, gorder, gcount, gsum;
+    // Muon: matrices, tiles of the symmetric products and of X, the region
+    // the runs share
+    size_t mats, sym, full, muon;
 };
 
 // Quantization maps.  A normalised magnitude a in [0, 1] maps to the largest
@@ -332,6 +366,18 @@ int64_t finite_pass_grid(int64_t nunits, int64_t tile, int32_t grid_request);
 int64_t norm_partials(int64_t nunits, int64_t tile, int32_t grid_request);
 hipError_t launch_grad_norm(const StepArgs &a, int gk, const float *inv_scale, double max_norm,
                             float *norm_out, float *clip_out, hipStream_t s);
+// Muon (kernels_muon.hip)
+struct MuonArgs {
+    const MuonMat *mats;
+    const MuonTile *sym, *full;
+    char *ws;             // the region the runs share
+    int32_t mat0, mat1;   // this run's matrices
+    float qa, qb, qc;     // the quintic
+    int32_t scale_kind;
+};
+hipError_t launch_muon(const StepArgs &a, const MuonArgs &ma, int pk, int gk, int32_t steps, int32_t nesterov,
+                       const MuonRun *runs, int32_t nruns, hipStream_t s);
+
 // Gradient lists (kernels_grads.hip).  kind: OPTIM_NORM_*.
 struct GradArgs {
     const GradTensor *tensors;
