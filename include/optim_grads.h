@@ -71,6 +71,39 @@ int optim_clip_coef(const float *norms_dev, int64_t count, int32_t kind,
 int optim_clip_grads(optim_plan *plan, const float *coef_dev,
                      const float *found_inf_dev, void *stream);
 
+/* ---- experts' weight gradients -------------------------------------------
+ * The weight gradients of a layer of experts, Y_e = X_e W_e, from the rows
+ * routed to each, sorted by expert: with X [tokens, m] and dY [tokens, n]
+ * (rows ldx and ldy elements apart, in_dtype BF16 or F16) and expert e's rows
+ * [offsets_dev[e], offsets_dev[e + 1]),
+ *   dW_e = s X_e^T dY_e            (accumulate 0)
+ *   dW_e = dW_e + s X_e^T dY_e     (otherwise)
+ * for dW [experts, m, n] (dw_dtype F32 or BF16, rows and experts end to end),
+ * s = *scale_dev (NULL: 1).  Products on the matrix cores, sums in fp32, one
+ * rounding to dw_dtype.  It fills gradients that the plans of a step, of
+ * optim_grad_norms and of optim_clip_grads read; accumulating over the
+ * micro-batches of a step into fp32 loses nothing to 16 bits in between.
+ * An expert without rows gets zeros (or keeps dW_e).  offsets_dev (device
+ * int32[experts + 1]) is read by the kernel, so routing needs no host
+ * synchronisation; each bound is clamped to [0, tokens] and to the one before
+ * it.  Rows outside every run are not read.
+ * Runs are summed in one piece, or, where the tiles of dW are too few to fill
+ * the GPU, in pieces through `workspace` (device, 256-byte aligned,
+ * optim_expert_grad_workspace bytes, contents free between calls); NULL
+ * sums in one piece, too few bytes are OPTIM_EWORKSPACE.  Either way the order of
+ * sums is fixed by the sizes: results repeat bit for bit.
+ * experts, tokens < 2^31; m, n < 2^24; ldx >= m, ldy >= n.  dW must not
+ * overlap X, dY or the workspace.  16-byte aligned X and dY with m, n, ldx
+ * and ldy multiples of 8 take the fastest path.                            */
+int optim_expert_grad_workspace(int32_t experts, int64_t tokens, int64_t m,
+                                int64_t n, size_t *bytes);
+int optim_expert_grad(const void *x_dev, int64_t ldx, const void *dy_dev,
+                      int64_t ldy, int32_t in_dtype, const int32_t *offsets_dev,
+                      int32_t experts, int64_t tokens, int64_t m, int64_t n,
+                      void *dw_dev, int32_t dw_dtype, int32_t accumulate,
+                      const float *scale_dev, void *workspace,
+                      size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -37,7 +37,8 @@ EXPORTED = (
     "optim_plan_create_static", "optim_plan_trace", "optim_plan_trace_read",
 )
 # entry points of include/optim_grads.h
-EXPORTED_GRADS = ("optim_grad_norms", "optim_clip_coef", "optim_clip_grads")
+EXPORTED_GRADS = ("optim_grad_norms", "optim_clip_coef", "optim_clip_grads", "optim_expert_grad_workspace",
+                  "optim_expert_grad")
 # entry points of include/optim_muon.h
 EXPORTED_MUON = ("optim_step_muon",)
 # bytes of the library's static per-device workspace (optim_plan_create_static)
@@ -150,6 +151,8 @@ def lib() -> ctypes.CDLL:
             "optim_grad_norms": ([_P, i32, _P, f64, _P, _P, _P, _P, _P], i32),
             "optim_clip_coef": ([_P, i64, i32, _P, f64, _P, _P, _P], i32),
             "optim_clip_grads": ([_P, _P, _P, _P], i32),
+            "optim_expert_grad_workspace": ([i32, i64, i64, i64, ctypes.POINTER(sz)], i32),
+            "optim_expert_grad": ([_P, i64, _P, i64, i32, _P, i32, i64, i64, i64, _P, i32, i32, _P, _P, sz, _P], i32),
         }
         for name, (args, res) in sigs.items():
             fn = getattr(L, name)
@@ -378,6 +381,43 @@ def optim_clip_coef(norms_dev, count: int, kind: int, inv_scale_dev, max_norm: f
 
 def optim_clip_grads(plan, coef_dev, found_inf_dev=None, stream=None) -> None:
     _check(lib().optim_clip_grads(plan, _ptr(coef_dev), _ptr(found_inf_dev), _stream(stream)), "optim_clip_grads")
+
+
+def optim_expert_grad_workspace(experts: int, tokens: int, m: int, n: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().optim_expert_grad_workspace(int(experts), int(tokens), int(m), int(n), ctypes.byref(out)),
+           "optim_expert_grad_workspace")
+    return out.value
+
+
+def _rows(t, what: str):
+    """Address and row distance of a matrix whose rows are contiguous."""
+    if t.dim() != 2 or (t.size(1) > 1 and t.stride(1) != 1) or (t.size(0) > 1 and t.stride(0) < t.size(1)):
+        raise ValueError(f"{what}: expected a matrix with contiguous rows, got shape {tuple(t.shape)} with strides "
+                         f"{t.stride()}")
+    if not t.is_cuda:
+        raise ValueError(f"{what}: expected a GPU tensor, got one on {t.device}")
+    return t.data_ptr(), max(t.stride(0) if t.size(0) > 1 else 0, t.size(1))
+
+
+def optim_expert_grad(x, dy, offsets, dw, *, accumulate: bool = False, scale=None, workspace=None, stream=None) -> None:
+    """x [tokens, m], dy [tokens, n] (bfloat16 or float16, rows may lie apart),
+    offsets int32 [experts + 1], dw [experts, m, n] (float32 or bfloat16),
+    workspace: a tensor of at least optim_expert_grad_workspace bytes."""
+    import torch
+    codes = {torch.float32: OPTIM_F32, torch.bfloat16: OPTIM_BF16, torch.float16: OPTIM_F16}
+    if x.dtype != dy.dtype or x.dtype not in codes or dw.dtype not in codes or offsets.dtype != torch.int32:
+        raise ValueError(f"expected x and dy of one 16-bit type, dw float32 or bfloat16 and int32 offsets, got {x.dtype}, "
+                         f"{dy.dtype}, {dw.dtype}, {offsets.dtype}")
+    if (dw.dim() != 3 or offsets.dim() != 1 or x.dim() != 2 or dy.dim() != 2 or x.size(0) != dy.size(0)
+            or tuple(dw.shape) != (offsets.numel() - 1, x.size(1), dy.size(1))):
+        raise ValueError(f"shapes do not fit: x {tuple(x.shape)}, dy {tuple(dy.shape)}, offsets {tuple(offsets.shape)}, "
+                         f"dw {tuple(dw.shape)}")
+    (px, ldx), (py, ldy) = _rows(x, "x"), _rows(dy, "dy")
+    nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(lib().optim_expert_grad(px, ldx, py, ldy, codes[x.dtype], _ptr(offsets), dw.size(0), x.size(0), x.size(1),
+                                   dy.size(1), _ptr(dw), codes[dw.dtype], int(accumulate), _ptr(scale), _ptr(workspace),
+                                   nbytes, _stream(stream)), "optim_expert_grad")
 
 
 def optim_scaler_update(scale_dev, inv_scale_dev, growth_tracker_dev, found_inf_dev, growth_factor: float,

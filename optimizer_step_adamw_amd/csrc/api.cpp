@@ -1111,6 +1111,19 @@ int check_muon_hp(const optim_muon_hp *hp) {
     return OPTIM_OK;
 }
 
+constexpr int64_t kExpertMaxSide = (int64_t(1) << 24) - 1;
+
+int check_expert_sizes(int32_t experts, int64_t tokens, int64_t m, int64_t n) {
+    if (experts < 0 || tokens < 0 || m < 0 || n < 0) return fail(OPTIM_EINVAL, "negative size");
+    if (tokens > INT32_MAX) return fail(OPTIM_EINVAL, "tokens must be below 2^31");
+    if (m > kExpertMaxSide || n > kExpertMaxSide) return fail(OPTIM_EINVAL, "m and n must be below 2^24");
+    // tiles are counted in 32 bits, elements of dW in 48
+    const int64_t tiles = ((m + 127) / 128) * ((n + 127) / 128);
+    if (experts > 0 && (tiles > (int64_t(1) << 26) / experts || (m > 0 && n > kMaxNumel / m / experts)))
+        return fail(OPTIM_EUNSUPPORTED, "dW has too many elements");
+    return OPTIM_OK;
+}
+
 GradArgs grad_args(optim_plan *P) {
     GradArgs a{};
     a.tensors = reinterpret_cast<const GradTensor *>(P->ws + P->L.gtensors);
@@ -1362,6 +1375,74 @@ int optim_clip_grads(optim_plan *plan, const float *coef_dev, const float *found
     if (!aligned(found_inf_dev, 4)) return fail(OPTIM_EALIGN, "scalar pointer misaligned");
     const TraceScope ts(plan);
     HIP_OK(launch_clip_grads(grad_args(plan), plan->gk, coef_dev, found_inf_dev, static_cast<hipStream_t>(stream)));
+    return OPTIM_OK;
+}
+
+int optim_expert_grad_workspace(int32_t experts, int64_t tokens, int64_t m, int64_t n, size_t *bytes) {
+    if (!bytes) return fail(OPTIM_EINVAL, "bytes is NULL");
+    if (const int rc = check_expert_sizes(experts, tokens, m, n)) return rc;
+    const int32_t pieces = expert_pieces(experts, tokens, m, n);
+    *bytes = pieces > 1 ? (size_t)pieces * experts * m * n * sizeof(float) : 0;
+    return OPTIM_OK;
+}
+
+int optim_expert_grad(const void *x_dev, int64_t ldx, const void *dy_dev, int64_t ldy, int32_t in_dtype,
+                      const int32_t *offsets_dev, int32_t experts, int64_t tokens, int64_t m, int64_t n, void *dw_dev,
+                      int32_t dw_dtype, int32_t accumulate, const float *scale_dev, void *workspace,
+                      size_t workspace_bytes, void *stream) {
+    if (const int rc = check_expert_sizes(experts, tokens, m, n)) return rc;
+    if (in_dtype != OPTIM_BF16 && in_dtype != OPTIM_F16)
+        return fail(OPTIM_EDTYPE, "in_dtype must be OPTIM_BF16 or OPTIM_F16");
+    if (dw_dtype != OPTIM_F32 && dw_dtype != OPTIM_BF16)
+        return fail(OPTIM_EDTYPE, "dw_dtype must be OPTIM_F32 or OPTIM_BF16");
+    if (ldx < m || ldy < n || ldx > kExpertMaxSide || ldy > kExpertMaxSide)
+        return fail(OPTIM_EINVAL, "ldx and ldy must be at least m and n, and below 2^24");
+    if (experts == 0 || m == 0 || n == 0) return OPTIM_OK;
+    if (!offsets_dev || !dw_dev || (tokens > 0 && (!x_dev || !dy_dev))) return fail(OPTIM_EINVAL, "NULL buffer");
+    const size_t osz = dw_dtype == OPTIM_F32 ? 4 : 2;
+    if (!aligned(x_dev, 2) || !aligned(dy_dev, 2) || !aligned(offsets_dev, 4) || !aligned(dw_dev, osz) ||
+        !aligned(scale_dev, 4))
+        return fail(OPTIM_EALIGN, "buffer misaligned");
+    int32_t pieces = workspace ? expert_pieces(experts, tokens, m, n) : 1;
+    const size_t need = pieces > 1 ? (size_t)pieces * experts * m * n * sizeof(float) : 0;
+    if (need) {
+        if (!aligned(workspace, 256))
+            return fail(OPTIM_EWORKSPACE, "workspace must be a 256-byte aligned device pointer");
+        if (workspace_bytes < need)
+            return fail(OPTIM_EWORKSPACE, "workspace too small: need " + std::to_string(need) + " bytes, got " +
+                                              std::to_string(workspace_bytes));
+    }
+    std::vector<Range> ranges;
+    auto add = [&](const void *p, size_t bytes, bool written, const char *what) {
+        if (p && bytes) ranges.push_back({(uintptr_t)p, (uintptr_t)p + bytes, written, 0, what});
+    };
+    if (tokens > 0) {
+        add(x_dev, ((size_t)(tokens - 1) * ldx + m) * 2, false, "x");
+        add(dy_dev, ((size_t)(tokens - 1) * ldy + n) * 2, false, "dy");
+    }
+    add(offsets_dev, ((size_t)experts + 1) * 4, false, "offsets");
+    add(dw_dev, (size_t)experts * m * n * osz, true, "dw");
+    add(need ? workspace : nullptr, need, true, "workspace");
+    if (const int rc = check_overlaps(ranges)) return rc;
+    ExpertArgs a{};
+    a.x = static_cast<const char *>(x_dev);
+    a.dy = static_cast<const char *>(dy_dev);
+    a.ldx = ldx * 2;
+    a.ldy = ldy * 2;
+    a.offsets = offsets_dev;
+    a.dw = static_cast<char *>(dw_dev);
+    a.parts = need ? static_cast<float *>(workspace) : nullptr;
+    a.scale = scale_dev;
+    a.experts = experts;
+    a.tokens = (int32_t)tokens;
+    a.m = (int32_t)m;
+    a.n = (int32_t)n;
+    a.pieces = pieces;
+    a.accumulate = accumulate != 0;
+    a.out_vec = n % 4 == 0 && aligned(dw_dev, 4 * osz);
+    const bool direct = m % 8 == 0 && n % 8 == 0 && ldx % 8 == 0 && ldy % 8 == 0 && aligned(x_dev, 16) && aligned(dy_dev, 16);
+    HIP_OK(launch_expert_grad(a, in_dtype == OPTIM_BF16, dw_dtype == OPTIM_F32, direct,
+                              static_cast<hipStream_t>(stream)));
     return OPTIM_OK;
 }
 

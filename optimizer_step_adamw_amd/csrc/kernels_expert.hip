@@ -1,0 +1,258 @@
+// kernels_expert.hip -- the weight gradients of a mixture of experts
+// (optim_expert_grad): dW_e (+)= s X_e^T dY_e, one product per expert over
+// its own run of rows.
+//
+// A workgroup computes a 128 x 128 tile of one expert's dW with the product of
+// tiles.h, both operands' k (the rows) running down memory.  Whole steps of 64
+// rows go straight from global memory into LDS; the rows left over, and every
+// step where a row is not a whole number of aligned 16-byte chunks, pass
+// through registers, where what lies outside the run or the matrix becomes
+// zero.
+#include "optim_grads.h"
+
+#include "tiles.h"
+
+#include <algorithm>
+
+namespace optim {
+namespace {
+
+constexpr int kStepRows = 64;
+// Tiles are taken in blocks of kBand x kBand of one expert, each block by
+// one XCD (workgroup b runs on XCD b mod 8), whose L2 then holds the
+// block's operands, and consecutive blocks by different XCDs, so that an
+// expert with many rows is spread over all of them.
+constexpr int kXcds = 8, kBand = 4, kGroup = kBand * kBand;
+
+// One operand's 64 x 128 tile from row k0 on, through registers: 4 chunks of
+// 8 values per lane.
+struct Chunks {
+    s16x8 v[4];
+};
+typedef s16x8 __attribute__((aligned(2))) s16x8_any;
+__device__ __forceinline__ Chunks load_chunks(const char *src, int64_t ld, int32_t rows, int32_t cols) {
+    Chunks r;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        int row, chunk;
+        feed_slot<KR, false>(t, row, chunk);
+        const int32_t left = cols - chunk * 8;
+        s16x8 v = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (row < rows && left > 0) {
+            const char *p = src + row * ld + chunk * 16;
+            if (left >= 8) {
+                v = *(const GMEM s16x8_any *)gp(p);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 7; ++i)
+                    if (i < left) v[i] = ((const GMEM short *)gp(p))[i];
+            }
+        }
+        r.v[t] = v;
+    }
+    return r;
+}
+__device__ __forceinline__ void write_chunks(const Chunks &r, char *lds) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+        *(LMEM s16x8 *)(lds + ((threadIdx.x >> 6) * 4 + t) * 1024 + (threadIdx.x & 63) * 16) = r.v[t];
+}
+
+template <bool F32>
+__device__ __forceinline__ float dw_get(const char *p, int64_t e) {
+    if constexpr (F32) return gp(reinterpret_cast<const float *>(p))[e];
+    else return bf16_to_f32(gp(reinterpret_cast<const uint16_t *>(p))[e]);
+}
+template <bool F32>
+__device__ __forceinline__ void dw_put(char *p, int64_t e, float x) {
+    if constexpr (F32) gp(reinterpret_cast<float *>(p))[e] = x;
+    else gp(reinterpret_cast<uint16_t *>(p))[e] = (uint16_t)f32_to_bf16_rne(x);
+}
+
+// Up to 4 neighbouring elements of dW from x, scaled and accumulated.
+template <bool F32>
+__device__ __forceinline__ void dw_store(const ExpertArgs &a, int64_t e, int n, f32x4 x, float s) {
+    if (a.out_vec) {  // (n is 4: a row is a multiple of 4)
+        if constexpr (F32) {
+            GMEM f32x4 *q = (GMEM f32x4 *)gp(a.dw + e * 4);
+            f32x4 y = x * s;
+            if (a.accumulate) y = *q + y;
+            *q = y;
+        } else {
+            GMEM u32x2 *q = (GMEM u32x2 *)gp(a.dw + e * 2);
+            float y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] = x[i] * s;
+            if (a.accumulate) {
+                const u32x2 old = *q;
+                y[0] += bf16_to_f32(old.x & 0xFFFFu);
+                y[1] += bf16_to_f32(old.x >> 16);
+                y[2] += bf16_to_f32(old.y & 0xFFFFu);
+                y[3] += bf16_to_f32(old.y >> 16);
+            }
+            *q = u32x2{f32_to_bf16_rne(y[0]) | f32_to_bf16_rne(y[1]) << 16,
+                       f32_to_bf16_rne(y[2]) | f32_to_bf16_rne(y[3]) << 16};
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < n) {
+            float y = x[i] * s;
+            if (a.accumulate) y = dw_get<F32>(a.dw, e + i) + y;
+            dw_put<F32>(a.dw, e + i, y);
+        }
+}
+
+// The rows of expert e's run that piece `piece` sums: whole steps of 64 but
+// for the last.
+__device__ __forceinline__ void expert_run(const ExpertArgs &a, int32_t e, int32_t piece, int32_t &k0, int32_t &k1) {
+    int32_t b = a.offsets[e], c = a.offsets[e + 1];
+    b = b < 0 ? 0 : (b < a.tokens ? b : a.tokens);
+    c = c < b ? b : (c < a.tokens ? c : a.tokens);
+    const int32_t steps = (int32_t)(((int64_t)c - b + kStepRows - 1) / kStepRows);
+    const int32_t each = (steps + a.pieces - 1) / a.pieces;
+    const int64_t lo = b + (int64_t)piece * each * kStepRows, hi = lo + (int64_t)each * kStepRows;
+    k0 = (int32_t)(lo < c ? lo : c);
+    k1 = (int32_t)(hi < c ? hi : c);
+}
+
+template <bool BF16, bool F32, bool DIRECT>
+__global__ __launch_bounds__(kThreads, 2) void expert_grad_kernel(ExpertArgs a) {
+    __shared__ __align__(1024) char lds[2 * kStageBytes];
+    // workgroup -> piece, expert, tile
+    const uint32_t b = blockIdx.x, slot = b / kXcds;
+    const uint32_t group = slot / kGroup * kXcds + b % kXcds, in = slot % kGroup;
+    const uint32_t gm = (a.mt + kBand - 1) / kBand, gn = (a.nt + kBand - 1) / kBand;
+    const uint32_t per = gm * gn, whole = group / per;
+    if (whole >= (uint32_t)a.experts * (uint32_t)a.pieces) return;
+    const int32_t e = (int32_t)(whole % (uint32_t)a.experts), piece = (int32_t)(whole / (uint32_t)a.experts);
+    const int32_t ti = (int32_t)(group % per / gn * kBand + in / kBand), tj = (int32_t)(group % per % gn * kBand + in % kBand);
+    if (ti >= a.mt || tj >= a.nt) return;
+    int32_t k0, k1;
+    expert_run(a, e, piece, k0, k1);
+    if (k0 >= k1 && a.accumulate && !a.parts) return;
+    const int32_t mleft = a.m - ti * kTile, nleft = a.n - tj * kTile;
+    const char *x = a.x + k0 * a.ldx + (int64_t)ti * kTile * 2, *y = a.dy + k0 * a.ldy + (int64_t)tj * kTile * 2;
+    const int32_t rows = k1 - k0;
+    Sums s{};
+    int32_t done = 0;
+    if constexpr (DIRECT) {
+        const int steps = rows / kStepRows;
+        product<KR, KR, false, BF16>(feed<KR, false>(x, a.ldx, mleft / 8), kStepRows * a.ldx,
+                                     feed<KR, false>(y, a.ldy, nleft / 8), kStepRows * a.ldy, steps, lds, s);
+        done = steps * kStepRows;
+        __syncthreads();
+    }
+    if (done < rows) {
+        Chunks cx = load_chunks(x + done * a.ldx, a.ldx, rows - done, mleft);
+        Chunks cy = load_chunks(y + done * a.ldy, a.ldy, rows - done, nleft);
+        write_chunks(cx, lds);
+        write_chunks(cy, lds + kOperandBytes);
+        for (int32_t half = 0;; half ^= 1) {
+            char *now = lds + half * kStageBytes, *next = lds + (half ^ 1) * kStageBytes;
+            __syncthreads();
+            Fragments f;
+            fragments<KR, KR, false>(now, f);
+            done += kStepRows;
+            const bool more = done < rows;
+            if (more) {
+                cx = load_chunks(x + done * a.ldx, a.ldx, rows - done, mleft);
+                cy = load_chunks(y + done * a.ldy, a.ldy, rows - done, nleft);
+            }
+            multiply<false, BF16>(f, s);
+            if (!more) break;
+            write_chunks(cx, next);
+            write_chunks(cy, next + kOperandBytes);
+        }
+    }
+    const float sc = a.scale ? *a.scale : 1.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int32_t r = ti * kTile + row0() + 16 * j, c = tj * kTile + col0() + 16 * i;
+            if (r >= a.m || c >= a.n) continue;
+            const int32_t n = a.n - c < 4 ? a.n - c : 4;
+            const int64_t at = ((int64_t)e * a.m + r) * a.n + c;
+            if (a.parts) {
+                float *q = a.parts + ((int64_t)piece * a.experts * a.m) * a.n + at;
+                if ((a.n & 3) == 0) {
+                    *(GMEM f32x4 *)gp(q) = s.v[i][j];
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (k < n) gp(q)[k] = s.v[i][j][k];
+                }
+            } else {
+                dw_store<F32>(a, at, n, s.v[i][j], sc);
+            }
+        }
+}
+
+// The pieces' sums in their order.
+template <bool F32>
+__global__ __launch_bounds__(kThreads) void expert_join_kernel(ExpertArgs a) {
+    const int64_t total = (int64_t)a.experts * a.m * a.n;
+    const float sc = a.scale ? *a.scale : 1.0f;
+    for (int64_t e = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4; e < total; e += (int64_t)gridDim.x * kThreads * 4) {
+        const int n = total - e < 4 ? (int)(total - e) : 4;
+        f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int32_t p = 0; p < a.pieces; ++p) {
+            const float *q = a.parts + (int64_t)p * total + e;
+            if ((total & 3) == 0) {
+                x = x + *(const GMEM f32x4 *)gp(q);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i < n) x[i] += gp(q)[i];
+            }
+        }
+        dw_store<F32>(a, e, n, x, sc);
+    }
+}
+
+template <bool BF16, bool F32>
+void launch_expert_t(const ExpertArgs &a, bool direct, unsigned grid, hipStream_t s) {
+    if (direct)
+        hipLaunchKernelGGL((expert_grad_kernel<BF16, F32, true>), dim3(grid), dim3(kThreads), 0, s, a);
+    else
+        hipLaunchKernelGGL((expert_grad_kernel<BF16, F32, false>), dim3(grid), dim3(kThreads), 0, s, a);
+    if (a.parts) {
+        const int64_t quads = ((int64_t)a.experts * a.m * a.n + 3) / 4;
+        const int64_t g = (quads + kThreads - 1) / kThreads;
+        hipLaunchKernelGGL((expert_join_kernel<F32>), dim3((unsigned)(g < 4096 ? g : 4096)), dim3(kThreads), 0, s, a);
+    }
+}
+
+int32_t tiles_of(int64_t n) { return (int32_t)((n + kTile - 1) / kTile); }
+
+}  // namespace
+
+// Two workgroups fit a compute unit, 512 the GPU.  Fewer tiles than that with
+// runs of many steps are summed in pieces of at least 8 steps (an even share
+// of the rows) until about 512 workgroups have work.
+int32_t expert_pieces(int32_t experts, int64_t tokens, int64_t m, int64_t n) {
+    if (experts <= 0 || m <= 0 || n <= 0) return 1;
+    const int64_t tiles = (int64_t)experts * tiles_of(m) * tiles_of(n);
+    const int64_t steps = tokens / experts / kStepRows;
+    const int64_t p = std::min<int64_t>(512 / tiles, steps / 8);
+    return (int32_t)(p < 1 ? 1 : p);
+}
+
+hipError_t launch_expert_grad(const ExpertArgs &args, bool bf16, bool out_f32, bool direct, hipStream_t s) {
+    ExpertArgs a = args;
+    a.mt = tiles_of(a.m);
+    a.nt = tiles_of(a.n);
+    const int64_t per = (int64_t)((a.mt + kBand - 1) / kBand) * ((a.nt + kBand - 1) / kBand);
+    const int64_t groups = per * a.experts * a.pieces;
+    const int64_t grid = (groups + kXcds - 1) / kXcds * kXcds * kGroup;
+    if (grid > INT32_MAX) return hipErrorInvalidValue;
+    if (bf16 && out_f32) launch_expert_t<true, true>(a, direct, (unsigned)grid, s);
+    else if (bf16) launch_expert_t<true, false>(a, direct, (unsigned)grid, s);
+    else if (out_f32) launch_expert_t<false, true>(a, direct, (unsigned)grid, s);
+    else launch_expert_t<false, false>(a, direct, (unsigned)grid, s);
+    return hipGetLastError();
+}
+
+}  // namespace optim

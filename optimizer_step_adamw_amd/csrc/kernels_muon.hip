@@ -198,11 +198,13 @@ __global__ __launch_bounds__(kThreads, 2) void muon_gram_kernel(StepArgs a, Muon
     const int64_t row = 4 * (int64_t)M.ld;  // bytes
     Sums s{};
     if (M.tall)
-        product<KR, KR, true, false>(X + (int64_t)t.i * kTile * 4, row, 32 * row, X + (int64_t)t.j * kTile * 4, row,
-                                     32 * row, (M.rows + 31) / 32, lds, s);
+        product<KR, KR, true, false>(feed<KR, true>(X + (int64_t)t.i * kTile * 4, row), 32 * row,
+                                     feed<KR, true>(X + (int64_t)t.j * kTile * 4, row), 32 * row, (M.rows + 31) / 32,
+                                     lds, s);
     else
-        product<KC, KC, true, false>(X + (int64_t)t.i * kTile * row, row, 128, X + (int64_t)t.j * kTile * row, row, 128,
-                                     (M.cols + 31) / 32, lds, s);
+        product<KC, KC, true, false>(feed<KC, true>(X + (int64_t)t.i * kTile * row, row), 128,
+                                     feed<KC, true>(X + (int64_t)t.j * kTile * row, row), 128, (M.cols + 31) / 32, lds,
+                                     s);
     store_symmetric(ma.ws + M.a, M.sp, t.i, t.j, [&](int i, int j, int64_t, int64_t, float(&x)[4]) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[e] = s.v[i][j][e] * kMuonUnscale;
@@ -218,7 +220,8 @@ __global__ __launch_bounds__(kThreads, 2) void muon_square_kernel(StepArgs a, Mu
     const char *A = ma.ws + M.a;
     const int64_t row = 4 * (int64_t)M.sp;
     Sums s{};
-    product<KC, KC, true, false>(A + (int64_t)t.i * kTile * row, row, 128, A + (int64_t)t.j * kTile * row, row, 128,
+    product<KC, KC, true, false>(feed<KC, true>(A + (int64_t)t.i * kTile * row, row), 128,
+                                 feed<KC, true>(A + (int64_t)t.j * kTile * row, row), 128,
                                  ((M.tall ? M.cols : M.rows) + 31) / 32, lds, s);
     store_symmetric(ma.ws + M.b, M.sp, t.i, t.j, [&](int i, int j, int64_t r, int64_t c, float(&x)[4]) {
         load_split4(A, split_at(r, c, M.sp), x);
@@ -233,11 +236,13 @@ __device__ __forceinline__ void apply_product(const MuonArgs &ma, const MuonTile
     const int64_t xrow = 4 * (int64_t)M.ld, brow = 4 * (int64_t)M.sp;
     const char *B = ma.ws + M.b;
     if (M.tall)
-        product<KC, KC, true, false>(X + (int64_t)t.i * kTile * xrow, xrow, 128, B + (int64_t)t.j * kTile * brow, brow,
-                                     128, (M.cols + 31) / 32, lds, s);
+        product<KC, KC, true, false>(feed<KC, true>(X + (int64_t)t.i * kTile * xrow, xrow), 128,
+                                     feed<KC, true>(B + (int64_t)t.j * kTile * brow, brow), 128, (M.cols + 31) / 32, lds,
+                                     s);
     else
-        product<KC, KR, true, false>(B + (int64_t)t.i * kTile * brow, brow, 128, X + (int64_t)t.j * kTile * 4, xrow,
-                                     32 * xrow, (M.rows + 31) / 32, lds, s);
+        product<KC, KR, true, false>(feed<KC, true>(B + (int64_t)t.i * kTile * brow, brow), 128,
+                                     feed<KR, true>(X + (int64_t)t.j * kTile * 4, xrow), 32 * xrow, (M.rows + 31) / 32,
+                                     lds, s);
 }
 
 __global__ __launch_bounds__(kThreads, 2) void muon_apply_kernel(StepArgs a, MuonArgs ma, int32_t from) {

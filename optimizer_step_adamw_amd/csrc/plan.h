@@ -396,6 +396,22 @@ hipError_t launch_grad_norms(const GradArgs &a, int gk, int kind, const float *i
 hipError_t launch_clip_grads(const GradArgs &a, int gk, const float *coef, const float *found_inf, hipStream_t s);
 hipError_t launch_clip_coef(const float *norms, int64_t count, int kind, const float *inv_scale, double max_norm,
                             float *total, float *coef, hipStream_t s);
+// Experts' weight gradients (kernels_expert.hip)
+struct ExpertArgs {
+    const char *x, *dy;
+    int64_t ldx, ldy;     // bytes between rows
+    const int32_t *offsets;
+    char *dw;
+    float *parts;         // partial sums [pieces][experts][m][n], or NULL
+    const float *scale;
+    int32_t experts, tokens, m, n;
+    int32_t mt, nt;       // tiles of one expert's dW
+    int32_t pieces;       // pieces of a run
+    int32_t accumulate;
+    int32_t out_vec;      // four neighbouring elements of dW are one access
+};
+int32_t expert_pieces(int32_t experts, int64_t tokens, int64_t m, int64_t n);
+hipError_t launch_expert_grad(const ExpertArgs &a, bool bf16, bool out_f32, bool direct, hipStream_t s);
 hipError_t launch_scaler_update(float *scale, float *inv_scale, int32_t *tracker, const float *found_inf,
                                 double growth, double backoff, int32_t interval, hipStream_t s);
 hipError_t launch_quantize(const Codebook *cb, int bits, int block, int is_signed, const float *x,

@@ -56,29 +56,51 @@ __device__ __forceinline__ void split2(float x, _Float16 &hi, _Float16 &lo) {
 // groups of 16 lanes take 4 rows each, k = 8 g + (0..3) (+ 4).
 __device__ __forceinline__ int kr_swizzle(int k) { return 2 * ((k & 3) | ((k >> 3) & 1) << 2); }
 
-// Stages one step of one operand: 16 loads of 1 KB, 4 per wavefront.
-// src: the operand's first byte of this step (KC: row 0, this k; KR: this k's
-// first row, column 0); ld: bytes between rows.
+// One operand's loads into LDS: 16 of 1 KB per step, 4 per wavefront, each
+// lane 16 bytes from `base` + at[t].  base (the same in every lane) moves on
+// from step to step.
+struct Feed {
+    const char *base;
+    uint32_t at[4];
+};
+// Row (KC: of the operand; KR: along k) and 16-byte chunk of load t.
 template <Order O, bool SPLIT>
-__device__ __forceinline__ void stage(const char *src, int64_t ld, char *lds) {
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+__device__ __forceinline__ void feed_slot(int t, int &row, int &chunk) {
+    const int lane = threadIdx.x & 63, i = (threadIdx.x >> 6) * 4 + t;
+    if constexpr (O == KC) {        // 8 chunks a row
+        row = i * 8 + (lane >> 3);
+        chunk = (lane & 7) ^ (row & 7);
+    } else if constexpr (SPLIT) {   // 32 chunks a row, 32 rows
+        row = i * 2 + (lane >> 5);
+        chunk = (lane & 31) ^ kr_swizzle(row);
+    } else {                        // 16 chunks a row, 64 rows
+        row = i * 4 + (lane >> 4);
+        chunk = (lane & 15) ^ kr_swizzle(row);
+    }
+}
+// src: the operand's first byte (KC: row 0 of the tile; KR: column 0 of the
+// tile in the first row); ld: bytes between rows (128 rows stay below 2^32);
+// chunks: 16-byte chunks of a row that exist (KR plain: the last one stands in for those
+// behind it, whose columns are not stored).
+template <Order O, bool SPLIT>
+__device__ __forceinline__ Feed feed(const char *src, int64_t ld, int chunks = 32) {
+    Feed f;
+    f.base = uniform_ptr(src);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-        const int i = w * 4 + t;
         int row, chunk;
-        if constexpr (O == KC) {        // 8 chunks a row
-            row = i * 8 + (lane >> 3);
-            chunk = (lane & 7) ^ (row & 7);
-        } else if constexpr (SPLIT) {   // 32 chunks a row, 32 rows
-            row = i * 2 + (lane >> 5);
-            chunk = (lane & 31) ^ kr_swizzle(row);
-        } else {                        // 16 chunks a row, 64 rows
-            row = i * 4 + (lane >> 4);
-            chunk = (lane & 15) ^ kr_swizzle(row);
-        }
-        __builtin_amdgcn_global_load_lds((const GMEM uint32_t *)gp(src + row * ld + chunk * 16),
-                                         (LMEM uint32_t *)(lds + i * 1024), 16, 0, 0);
+        feed_slot<O, SPLIT>(t, row, chunk);
+        if (O == KR && !SPLIT && chunk >= chunks) chunk = chunks - 1;
+        f.at[t] = (uint32_t)(row * ld + chunk * 16);
     }
+    return f;
+}
+__device__ __forceinline__ void stage(const Feed &f, char *lds) {
+    const int w = threadIdx.x >> 6;
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+        __builtin_amdgcn_global_load_lds((const GMEM uint32_t *)gp(f.base + f.at[t]),
+                                         (LMEM uint32_t *)(lds + (w * 4 + t) * 1024), 16, 0, 0);
 }
 
 // The 16 x 32 fragment of rows (KC) or columns (KR) 16 b .. 16 b + 15; part:
@@ -154,27 +176,26 @@ __device__ __forceinline__ void staged() {
     __syncthreads();
 }
 
-// Sum over `steps` steps; step t's operands begin t * kp / t * kq bytes
-// further.  A step's fragments are read before the next step's loads into LDS
+// Sum over `steps` steps; an operand moves on by kp / kq bytes from step to
+// step.  A step's fragments are read before the next step's loads into LDS
 // are issued: the compiler cannot tell the two halves of the buffer apart and
 // would wait for those loads before the first read behind them.
 template <Order OP, Order OQ, bool SPLIT, bool BF16>
-__device__ __forceinline__ void product(const char *p, int64_t ldp, int64_t kp, const char *q, int64_t ldq, int64_t kq,
-                                        int steps, char *lds, Sums &s) {
+__device__ __forceinline__ void product(Feed p, int64_t kp, Feed q, int64_t kq, int steps, char *lds, Sums &s) {
     if (steps > 0) {
-        stage<OP, SPLIT>(p, ldp, lds);
-        stage<OQ, SPLIT>(q, ldq, lds + kOperandBytes);
+        stage(p, lds);
+        stage(q, lds + kOperandBytes);
     }
     for (int t = 0; t < steps; ++t) {
         char *now = lds + (t & 1) * kStageBytes, *next = lds + (~t & 1) * kStageBytes;
         staged();
         Fragments f;
         fragments<OP, OQ, SPLIT>(now, f);
-        p += kp;
-        q += kq;
+        p.base += kp;
+        q.base += kq;
         if (t + 1 < steps) {
-            stage<OP, SPLIT>(p, ldp, next);
-            stage<OQ, SPLIT>(q, ldq, next + kOperandBytes);
+            stage(p, next);
+            stage(q, next + kOperandBytes);
         }
         multiply<SPLIT, BF16>(f, s);
     }

@@ -88,3 +88,32 @@ def test_binding_refuses_mixed_and_unknown_types(L):
         osa.grad_list([torch.zeros(3, dtype=torch.float64)])
     with pytest.raises(ValueError):
         osa.grad_list([torch.zeros(3)])  # not on a GPU
+
+
+def test_expert_grad_refusals(L):
+    import ctypes
+    out = ctypes.c_size_t(0)
+    W = L.optim_expert_grad_workspace
+    assert W(4, 100, 64, 64, None) == osa.OPTIM_EINVAL
+    for bad in ((-1, 10, 8, 8), (1, -1, 8, 8), (1, 10, -8, 8), (1, 10, 8, -8), (1, 1 << 31, 8, 8), (1, 10, 1 << 24, 8)):
+        assert W(*bad, ctypes.byref(out)) == osa.OPTIM_EINVAL, bad
+    assert W(1 << 20, 10, 1 << 20, 1 << 20, ctypes.byref(out)) == osa.OPTIM_EUNSUPPORTED
+    assert W(64, 65536, 2048, 1024, ctypes.byref(out)) == osa.OPTIM_OK and out.value == 0
+    assert W(1, 65536, 128, 128, ctypes.byref(out)) == osa.OPTIM_OK and out.value > 0
+    assert W(0, 0, 0, 0, ctypes.byref(out)) == osa.OPTIM_OK and out.value == 0
+
+    def call(x=A, ldx=64, dy=A + (1 << 30), ldy=32, dt=osa.OPTIM_BF16, off=A + (2 << 30), e=2, t=100, m=64, n=32,
+             dw=A + (3 << 30), odt=osa.OPTIM_F32, scale=None, ws=None, nws=0):
+        return L.optim_expert_grad(x, ldx, dy, ldy, dt, off, e, t, m, n, dw, odt, 0, scale, ws, nws, None)
+
+    assert call(e=0) == call(m=0) == call(n=0, ldy=0) == osa.OPTIM_OK  # nothing to do, nothing launched
+    for kw in (dict(ldx=63), dict(ldy=31), dict(x=None), dict(dy=None), dict(off=None), dict(dw=None), dict(e=-1), dict(t=-1),
+               dict(dw=A + 64), dict(dw=A + (1 << 30)), dict(off=A + (3 << 30)), dict(ldx=1 << 24)):
+        assert call(**kw) == osa.OPTIM_EINVAL, kw
+    for kw in (dict(dt=osa.OPTIM_F32), dict(odt=osa.OPTIM_F16), dict(dt=5)):
+        assert call(**kw) == osa.OPTIM_EDTYPE, kw
+    for kw in (dict(x=A + 1), dict(dy=A + (1 << 30) + 1), dict(off=A + (2 << 30) + 2), dict(dw=A + (3 << 30) + 2), dict(scale=A + 3)):
+        assert call(**kw) == osa.OPTIM_EALIGN, kw
+    # a workspace that is too small or not aligned (the sizes want one)
+    assert call(t=65536, e=1, ws=A + (4 << 30), nws=1000) == osa.OPTIM_EWORKSPACE
+    assert call(t=65536, e=1, ws=A + (4 << 30) + 16, nws=1 << 30) == osa.OPTIM_EWORKSPACE
