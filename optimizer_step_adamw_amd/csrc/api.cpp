@@ -135,6 +135,7 @@ struct Built {
     std::vector<MuonTile> sym, full;
     std::vector<MuonRun> runs;
     int64_t muon_bytes = 0;         // of the region the runs share
+    int64_t muon_tiles = 0;
     Layout L{};
 };
 
@@ -172,27 +173,132 @@ int check_hp_beta(double b, const char *name) {
 
 bool is_blockwise(int32_t algo) { return algo == OPTIM_ALGO_BLOCKWISE || algo == OPTIM_ALGO_BLOCKWISE_ADEMAMIX; }
 
-int64_t pad_tile(int64_t n) { return (n + kMuonTile - 1) / kMuonTile * kMuonTile; }
+int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+// Whether a matrix may take wide tiles (in a plan with enough of them): below,
+// padding to whole wide tiles costs more than they gain.
+bool wide_matrix(int64_t rows, int64_t cols) { return std::min(rows, cols) >= kMuonWideMin; }
 
-// Muon: the matrices of tensor i, their arrays and tiles.  A run takes
+// Workgroup b runs on XCD b mod kXcds, each with an L2 of its own.
+constexpr int kXcds = 8;
+
+// Appends a run's tiles in launch order.  Blocks of up to 4 x 4 tiles of one
+// matrix (`block` numbers them) stay on one XCD, whose L2 then holds their
+// operands once; a block goes to the XCD with the fewest tiles, and single
+// tiles then move until all XCDs have as many (but for one: -1 fills up).  Few
+// tiles are spread over the XCDs one by one.
+void order_tiles(const std::vector<std::pair<int64_t, MuonTile>> &tiles, std::vector<MuonTile> &out) {
+    std::vector<MuonTile> of[kXcds];
+    const bool blocks = tiles.size() >= 512;
+    int x = 0;
+    for (size_t k = 0; k < tiles.size(); ++k) {
+        if (k == 0 || !blocks || tiles[k].first != tiles[k - 1].first) {
+            x = 0;
+            for (int y = 1; y < kXcds; ++y)
+                if (of[y].size() < of[x].size()) x = y;
+        }
+        of[x].push_back(tiles[k].second);
+    }
+    for (;;) {
+        int most = 0, least = 0;
+        for (int y = 1; y < kXcds; ++y) {
+            if (of[y].size() > of[most].size()) most = y;
+            if (of[y].size() < of[least].size()) least = y;
+        }
+        if (of[most].size() <= of[least].size() + 1) break;
+        of[least].push_back(of[most].back());
+        of[most].pop_back();
+    }
+    size_t longest = 0;
+    for (const auto &v : of) longest = std::max(longest, v.size());
+    for (size_t k = 0; k < longest; ++k)
+        for (const auto &v : of) out.push_back(k < v.size() ? v[k] : MuonTile{-1, 0, 0});
+    while (!out.empty() && out.back().mat < 0 && !tiles.empty()) out.pop_back();
+}
+
+// A run's tiles of one product, in whole rounds of wide tiles over the GPU and,
+// where they are at most half a round, the rest as four narrow tiles each: a
+// round of a few wide tiles takes as long as a full one.  upper: tiles on and
+// above the diagonal of square arrays.
+void add_product(const Built &B, const MuonRun &R, bool upper, std::vector<MuonTile> &out, int64_t &first,
+                 int64_t &wide, int64_t &narrow) {
+    typedef std::vector<std::pair<int64_t, MuonTile>> Tiles;
+    Tiles tiles, rest;
+    const int64_t tile = R.wide ? kMuonWideTile : kMuonTile;
+    int64_t block = 0;
+    for (int32_t m = R.mat0; m < R.mat1; ++m) {
+        const MuonMat &M = B.mats[m];
+        const int64_t rows = (upper ? M.sp : M.rp) / tile, cols = (upper ? M.sp : M.ld) / tile;
+        for (int64_t a = 0; a < rows; a += 4)
+            for (int64_t b = upper ? a : 0; b < cols; b += 4, ++block)
+                for (int64_t i = a; i < std::min(a + 4, rows); ++i)
+                    for (int64_t j = upper ? std::max(b, i) : b; j < std::min(b + 4, cols); ++j)
+                        tiles.push_back({block, MuonTile{m, (uint16_t)i, (uint16_t)j}});
+    }
+    first = (int64_t)out.size();
+    if (!R.wide) {
+        std::swap(tiles, rest);
+    } else {
+        const size_t over = tiles.size() % kMuonSlots;
+        if (over <= kMuonSlots / 2) {
+            for (size_t k = tiles.size() - over; k < tiles.size(); ++k) {
+                const MuonTile t = tiles[k].second;
+                for (int i = 0; i < 2; ++i)
+                    for (int j = upper && t.i == t.j ? i : 0; j < 2; ++j)
+                        rest.push_back({tiles[k].first, MuonTile{t.mat, (uint16_t)(2 * t.i + i), (uint16_t)(2 * t.j + j)}});
+            }
+            tiles.resize(tiles.size() - over);
+        }
+    }
+    order_tiles(tiles, out);
+    wide = (int64_t)out.size() - first;
+    order_tiles(rest, out);
+    narrow = (int64_t)out.size() - first - wide;
+}
+
+// The tile tables of the runs, from their matrices.  Plans whose products
+// have fewer narrow tiles than there are compute units give each tile two
+// groups of wavefronts.  (Decided for the plan, not run by run: the groups sum
+// in another order, and results do not depend on the bound on a run.)
+void add_tiles(Built &B) {
+    int64_t sym = 0, full = 0;
+    for (const MuonMat &M : B.mats) {
+        const int64_t nt = M.sp / kMuonTile;
+        sym += nt * (nt + 1) / 2;
+        full += (int64_t)(M.rp / kMuonTile) * (M.ld / kMuonTile);
+    }
+    for (MuonRun &R : B.runs) {
+        add_product(B, R, true, B.sym, R.sym0, R.wide_sym, R.nsym);
+        add_product(B, R, false, B.full, R.full0, R.wide_full, R.nfull);
+        R.pair_sym = sym <= kMuonSlots;
+        R.pair_full = full <= kMuonSlots;
+    }
+}
+
+// Muon: the matrices of tensor i and their arrays.  A run takes
 // matrices until their arrays pass `cap` bytes.
-int add_matrices(const std::string &ti, int i, int64_t numel, int64_t rows, int64_t cols, int64_t cap, Built &B) {
+int add_matrices(const std::string &ti, int i, int64_t numel, int64_t rows, int64_t cols, bool wide, int64_t cap,
+                 Built &B) {
     if (rows < 1 || cols < 1 || rows > kMuonMaxSide || cols > kMuonMaxSide)
         return fail(OPTIM_EINVAL, ti + "rows and cols must be in [1, 2^20]");
     if (numel % (rows * cols) != 0) return fail(OPTIM_EINVAL, ti + "numel must be a multiple of rows * cols");
     const int64_t count = numel / (rows * cols);
-    const int64_t rp = pad_tile(rows), ld = pad_tile(cols), sp = std::min(rp, ld);
+    const int64_t tile = wide ? kMuonWideTile : kMuonTile;
+    const int64_t rp = round_up(rows, tile), ld = round_up(cols, tile), sp = std::min(rp, ld);
     const int64_t bytes = 2 * (rp * ld * 4) + 2 * (sp * sp * 4);
-    const int64_t nt = sp / kMuonTile;
-    const int64_t tiles = nt * (nt + 1) / 2 + (rp / kMuonTile) * (ld / kMuonTile);
+    const int64_t nt = sp / tile;
+    const int64_t tiles = nt * (nt + 1) / 2 + (rp / tile) * (ld / tile);
     if (count > INT32_MAX / 4 || (int64_t)B.mats.size() + count > INT32_MAX / 4 ||
-        tiles > (((int64_t)1 << 26) - (int64_t)(B.sym.size() + B.full.size())) / count)
+        tiles > (((int64_t)1 << 26) - B.muon_tiles) / count)
         return fail(OPTIM_EUNSUPPORTED, ti + "too many matrices or tiles");
+    B.muon_tiles += tiles * count;
     for (int64_t k = 0; k < count; ++k) {
         int64_t used = B.mats.empty() ? 0 : B.mats.back().b + (int64_t)B.mats.back().sp * B.mats.back().sp * 4;
-        if (B.runs.empty() || used + bytes > cap) {
+        if (B.runs.empty() || B.runs.back().wide != (int32_t)wide || used + bytes > cap) {
             const int32_t m = (int32_t)B.mats.size();
-            B.runs.push_back(MuonRun{m, m, 0, (int64_t)B.sym.size(), 0, (int64_t)B.full.size(), 0});
+            MuonRun R{};
+            R.mat0 = R.mat1 = m;
+            R.wide = wide;
+            B.runs.push_back(R);
             used = 0;
         }
         MuonRun &R = B.runs.back();
@@ -212,14 +318,8 @@ int add_matrices(const std::string &ti, int i, int64_t numel, int64_t rows, int6
         M.tall = rows > cols;
         const int32_t m = (int32_t)B.mats.size();
         B.mats.push_back(M);
-        for (int64_t a = 0; a < nt; ++a)
-            for (int64_t b = a; b < nt; ++b) B.sym.push_back(MuonTile{m, (uint16_t)a, (uint16_t)b});
-        for (int64_t a = 0; a < rp / kMuonTile; ++a)
-            for (int64_t b = 0; b < ld / kMuonTile; ++b) B.full.push_back(MuonTile{m, (uint16_t)a, (uint16_t)b});
         R.mat1 = m + 1;
         R.units += rp * ld / kMuonUnit;
-        R.nsym = (int64_t)B.sym.size() - R.sym0;
-        R.nfull = (int64_t)B.full.size() - R.full0;
         B.muon_bytes = std::max(B.muon_bytes, used + bytes);
         // a span per matrix: its units' sums of squares give its norm
         B.blockspan.push_back((int32_t)B.spans.size());
@@ -605,7 +705,7 @@ int build(const optim_tensor_list *list, int32_t algo, const optim_plan_opts *op
                 ++B.nblocks;
             }
         } else if (muon) {
-            if (const int rc = add_matrices(ti, i, numel, list->rows[i], list->cols[i], seg_cap, B)) return rc;
+            // (their spans are added below, run by run)
         } else if (algo == OPTIM_ALGO_LAMB || states16) {
             // one block per tensor: its trust ratio, or its state scales
             B.blockspan.push_back((int32_t)B.spans.size());
@@ -639,6 +739,26 @@ int build(const optim_tensor_list *list, int32_t algo, const optim_plan_opts *op
             }
         }
     }
+    // Muon: wide tiles where all matrices that may take them make a round of
+    // the GPU; these matrices first, then the others, so that a run's matrices
+    // are of one kind
+    int64_t wide_full = 0;
+    for (int i = 0; muon && i < n; ++i) {
+        const int64_t r = list->rows[i], c = list->cols[i];
+        if (list->numel[i] > 0 && r > 0 && c > 0 && r <= kMuonMaxSide && c <= kMuonMaxSide && wide_matrix(r, c))
+            wide_full += list->numel[i] / (r * c) * (round_up(r, kMuonWideTile) / kMuonWideTile) *
+                         (round_up(c, kMuonWideTile) / kMuonWideTile);
+    }
+    for (int pass = 0; muon && pass < 2; ++pass)
+        for (int i = 0; i < n; ++i) {
+            if (list->numel[i] == 0) continue;
+            const int64_t r = list->rows[i], c = list->cols[i];
+            const bool wide = wide_full >= kMuonSlots && wide_matrix(r, c);
+            if (wide != (pass == 0)) continue;
+            if (const int rc = add_matrices("tensor " + std::to_string(i) + ": ", i, list->numel[i], r, c, wide, seg_cap, B))
+                return rc;
+        }
+    add_tiles(B);
     close_pack();
     B.pack_unit0 = B.nunits;
     for (size_t k = 0; k < B.packs.size(); ++k) {

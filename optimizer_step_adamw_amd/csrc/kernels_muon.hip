@@ -102,18 +102,27 @@ __device__ __forceinline__ int muon_find(const MuonArgs &a, int64_t u) {
 }
 
 // Four values of a split array as two 8-byte stores.
-__device__ __forceinline__ void store_split4(char *base, int64_t at, const float (&x)[4]) {
-    f16x4 hi, lo;
+__device__ __forceinline__ void split4(const float (&x)[4], uint2 &hi, uint2 &lo) {
+    f16x4 h, l;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        _Float16 h, l;
-        split2(x[i], h, l);
-        hi[i] = h;
-        lo[i] = l;
+        _Float16 a, b;
+        split2(x[i], a, b);
+        h[i] = a;
+        l[i] = b;
     }
-    GMEM f16x4 *q = (GMEM f16x4 *)gp(base + at * 2);
-    q[0] = hi;
-    q[8] = lo;
+    hi = __builtin_bit_cast(uint2, h);
+    lo = __builtin_bit_cast(uint2, l);
+}
+__device__ __forceinline__ void put_split4(char *base, int64_t at, uint2 hi, uint2 lo) {
+    GMEM u32x2 *q = (GMEM u32x2 *)gp(base + at * 2);
+    q[0] = u32x2{hi.x, hi.y};
+    q[8] = u32x2{lo.x, lo.y};
+}
+__device__ __forceinline__ void store_split4(char *base, int64_t at, const float (&x)[4]) {
+    uint2 hi, lo;
+    split4(x, hi, lo);
+    put_split4(base, at, hi, lo);
 }
 __device__ __forceinline__ void load_split4(const char *base, int64_t at, float (&x)[4]) {
     const GMEM f16x4 *q = (const GMEM f16x4 *)gp(base + at * 2);
@@ -163,67 +172,91 @@ __global__ __launch_bounds__(kThreads) void muon_split_kernel(StepArgs a, MuonAr
 }
 
 // ---------------------------------------------------------------- products
-// Stores this wavefront's 64 x 64 sums times f as part of tile (ti, tj) of
-// the symmetric array at `base`, and of tile (tj, ti).
-template <class F>
+// The operand whose rows (columns) are those of tile row (column) t.
+template <int W>
+__device__ __forceinline__ Feed row_feed(const char *base, int t, int64_t rows32) {
+    return feed<W, KC, true>(base + (int64_t)t * (Tile<W>::kSide / 32) * rows32, rows32);
+}
+template <int W>
+__device__ __forceinline__ Feed column_feed(const char *base, int t, int64_t rows32) {
+    return feed<W, KR, true>(base + (int64_t)t * (Tile<W>::kSide / 32) * kSplitBlock, rows32);
+}
+
+// Transposes a 4 x 4 block of 16-bit numbers held by 4 neighbouring lanes:
+// lane q's four (element e in half e % 2 of word e / 2) become element q of
+// the four lanes.
+__device__ __forceinline__ uint2 transpose4(uint2 d) {
+    const int q = threadIdx.x & 3;
+    // neighbours: halves of both words
+    const uint32_t x = (uint32_t)__builtin_amdgcn_mov_dpp((int)d.x, 0xB1, 0xF, 0xF, true);  // lane ^ 1
+    const uint32_t y = (uint32_t)__builtin_amdgcn_mov_dpp((int)d.y, 0xB1, 0xF, 0xF, true);
+    const uint32_t a = q & 1 ? (d.x & 0xFFFF0000u) | x >> 16 : (d.x & 0xFFFFu) | x << 16;
+    const uint32_t b = q & 1 ? (d.y & 0xFFFF0000u) | y >> 16 : (d.y & 0xFFFFu) | y << 16;
+    // pairs: whole words
+    const uint32_t give = q & 2 ? a : b, keep = q & 2 ? b : a;
+    const uint32_t take = (uint32_t)__builtin_amdgcn_mov_dpp((int)give, 0x4E, 0xF, 0xF, true);  // lane ^ 2
+    return q & 2 ? make_uint2(take, keep) : make_uint2(keep, take);
+}
+
+// Stores this wavefront's sums, through value(), as part of tile (ti, tj) of
+// the symmetric array at `base`, and transposed as part of tile (tj, ti).
+template <int W, bool PAIR, class F>
 __device__ __forceinline__ void store_symmetric(char *base, int64_t ld, int ti, int tj, F &&value) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < Tile<W, PAIR>::kOutJ; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int64_t r = (int64_t)ti * kTile + row0() + 16 * j, c = (int64_t)tj * kTile + col0() + 16 * i;
+            const int64_t r = (int64_t)ti * Tile<W>::kSide + row0<W, PAIR>() + 16 * j;
+            const int64_t c = (int64_t)tj * Tile<W>::kSide + col0<W>() + 16 * i;
             float x[4];
             value(i, j, r, c, x);
-            store_split4(base, split_at(r, c, ld), x);
-            if (ti != tj) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    _Float16 hi, lo;
-                    split2(x[e], hi, lo);
-                    GMEM _Float16 *q = (GMEM _Float16 *)gp(base + split_at(c + e, r, ld) * 2);
-                    q[0] = hi;
-                    q[32] = lo;
-                }
-            }
+            uint2 hi, lo;
+            split4(x, hi, lo);
+            put_split4(base, split_at(r, c, ld), hi, lo);
+            if (ti != tj)
+                put_split4(base, split_at(c + (threadIdx.x & 3), r & ~(int64_t)3, ld), transpose4(hi), transpose4(lo));
         }
 }
 
 // A = X X^T or X^T X
-__global__ __launch_bounds__(kThreads, 2) void muon_gram_kernel(StepArgs a, MuonArgs ma, int32_t from) {
-    __shared__ __align__(1024) char lds[2 * kStageBytes];
+template <int W, bool PAIR>
+__global__ __launch_bounds__((Tile<W, PAIR>::kLanes), (Tile<W, PAIR>::kWavesPerSimd)) void muon_gram_kernel(StepArgs a, MuonArgs ma, int32_t from) {
+    __shared__ __align__(1024) char lds[Tile<W, PAIR>::kLds];
     if (skipped(a)) return;
     const MuonTile t = ma.sym[blockIdx.x];
+    if (t.mat < 0) return;
     const MuonMat M = ma.mats[t.mat];
     const char *X = ma.ws + M.x[from];
-    const int64_t row = 4 * (int64_t)M.ld;  // bytes
-    Sums s{};
+    const int64_t rows32 = split_rows32(M.ld);
+    Sums<W> s{};
     if (M.tall)
-        product<KR, KR, true, false>(feed<KR, true>(X + (int64_t)t.i * kTile * 4, row), 32 * row,
-                                     feed<KR, true>(X + (int64_t)t.j * kTile * 4, row), 32 * row, (M.rows + 31) / 32,
-                                     lds, s);
+        product<W, PAIR, KR, KR, true, false>(column_feed<W>(X, t.i, rows32), rows32, column_feed<W>(X, t.j, rows32), rows32,
+                                           (M.rows + 31) / 32, lds_at(lds), s);
     else
-        product<KC, KC, true, false>(feed<KC, true>(X + (int64_t)t.i * kTile * row, row), 128,
-                                     feed<KC, true>(X + (int64_t)t.j * kTile * row, row), 128, (M.cols + 31) / 32, lds,
-                                     s);
-    store_symmetric(ma.ws + M.a, M.sp, t.i, t.j, [&](int i, int j, int64_t, int64_t, float(&x)[4]) {
+        product<W, PAIR, KC, KC, true, false>(row_feed<W>(X, t.i, rows32), kSplitBlock, row_feed<W>(X, t.j, rows32),
+                                           kSplitBlock, (M.cols + 31) / 32, lds_at(lds), s);
+    join_pair<W, PAIR>(lds_at(lds), s);
+    store_symmetric<W, PAIR>(ma.ws + M.a, M.sp, t.i, t.j, [&](int i, int j, int64_t, int64_t, float(&x)[4]) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[e] = s.v[i][j][e] * kMuonUnscale;
     });
 }
 
 // B = b A + c A A
-__global__ __launch_bounds__(kThreads, 2) void muon_square_kernel(StepArgs a, MuonArgs ma) {
-    __shared__ __align__(1024) char lds[2 * kStageBytes];
+template <int W, bool PAIR>
+__global__ __launch_bounds__((Tile<W, PAIR>::kLanes), (Tile<W, PAIR>::kWavesPerSimd)) void muon_square_kernel(StepArgs a, MuonArgs ma) {
+    __shared__ __align__(1024) char lds[Tile<W, PAIR>::kLds];
     if (skipped(a)) return;
     const MuonTile t = ma.sym[blockIdx.x];
+    if (t.mat < 0) return;
     const MuonMat M = ma.mats[t.mat];
     const char *A = ma.ws + M.a;
-    const int64_t row = 4 * (int64_t)M.sp;
-    Sums s{};
-    product<KC, KC, true, false>(feed<KC, true>(A + (int64_t)t.i * kTile * row, row), 128,
-                                 feed<KC, true>(A + (int64_t)t.j * kTile * row, row), 128,
-                                 ((M.tall ? M.cols : M.rows) + 31) / 32, lds, s);
-    store_symmetric(ma.ws + M.b, M.sp, t.i, t.j, [&](int i, int j, int64_t r, int64_t c, float(&x)[4]) {
+    const int64_t rows32 = split_rows32(M.sp);
+    Sums<W> s{};
+    product<W, PAIR, KC, KC, true, false>(row_feed<W>(A, t.i, rows32), kSplitBlock, row_feed<W>(A, t.j, rows32), kSplitBlock,
+                                       ((M.tall ? M.cols : M.rows) + 31) / 32, lds_at(lds), s);
+    join_pair<W, PAIR>(lds_at(lds), s);
+    store_symmetric<W, PAIR>(ma.ws + M.b, M.sp, t.i, t.j, [&](int i, int j, int64_t r, int64_t c, float(&x)[4]) {
         load_split4(A, split_at(r, c, M.sp), x);
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[e] = ma.qb * x[e] + ma.qc * (s.v[i][j][e] * kMuonUnscale);
@@ -231,34 +264,36 @@ __global__ __launch_bounds__(kThreads, 2) void muon_square_kernel(StepArgs a, Mu
 }
 
 // X <- a X + B X or a X + X B
+template <int W, bool PAIR>
 __device__ __forceinline__ void apply_product(const MuonArgs &ma, const MuonTile &t, const MuonMat &M, const char *X,
-                                              char *lds, Sums &s) {
-    const int64_t xrow = 4 * (int64_t)M.ld, brow = 4 * (int64_t)M.sp;
+                                              uint32_t lds, Sums<W> &s) {
+    const int64_t x32 = split_rows32(M.ld), b32 = split_rows32(M.sp);
     const char *B = ma.ws + M.b;
     if (M.tall)
-        product<KC, KC, true, false>(feed<KC, true>(X + (int64_t)t.i * kTile * xrow, xrow), 128,
-                                     feed<KC, true>(B + (int64_t)t.j * kTile * brow, brow), 128, (M.cols + 31) / 32, lds,
-                                     s);
+        product<W, PAIR, KC, KC, true, false>(row_feed<W>(X, t.i, x32), kSplitBlock, row_feed<W>(B, t.j, b32), kSplitBlock,
+                                           (M.cols + 31) / 32, lds, s);
     else
-        product<KC, KR, true, false>(feed<KC, true>(B + (int64_t)t.i * kTile * brow, brow), 128,
-                                     feed<KR, true>(X + (int64_t)t.j * kTile * 4, xrow), 32 * xrow, (M.rows + 31) / 32,
-                                     lds, s);
+        product<W, PAIR, KC, KR, true, false>(row_feed<W>(B, t.i, b32), kSplitBlock, column_feed<W>(X, t.j, x32), x32,
+                                           (M.rows + 31) / 32, lds, s);
+    join_pair<W, PAIR>(lds, s);
 }
 
-__global__ __launch_bounds__(kThreads, 2) void muon_apply_kernel(StepArgs a, MuonArgs ma, int32_t from) {
-    __shared__ __align__(1024) char lds[2 * kStageBytes];
+template <int W, bool PAIR>
+__global__ __launch_bounds__((Tile<W, PAIR>::kLanes), (Tile<W, PAIR>::kWavesPerSimd)) void muon_apply_kernel(StepArgs a, MuonArgs ma, int32_t from) {
+    __shared__ __align__(1024) char lds[Tile<W, PAIR>::kLds];
     if (skipped(a)) return;
     const MuonTile t = ma.full[blockIdx.x];
+    if (t.mat < 0) return;
     const MuonMat M = ma.mats[t.mat];
     const char *X = ma.ws + M.x[from];
     char *Y = ma.ws + M.x[from ^ 1];
-    Sums s{};
-    apply_product(ma, t, M, X, lds, s);
+    Sums<W> s{};
+    apply_product<W, PAIR>(ma, t, M, X, lds_at(lds), s);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < Tile<W, PAIR>::kOutJ; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int64_t at = split_at((int64_t)t.i * kTile + row0() + 16 * j, (int64_t)t.j * kTile + col0() + 16 * i, M.ld);
+            const int64_t at = split_at((int64_t)t.i * Tile<W>::kSide + row0<W, PAIR>() + 16 * j, (int64_t)t.j * Tile<W>::kSide + col0<W>() + 16 * i, M.ld);
             float x[4];
             load_split4(X, at, x);
 #pragma unroll
@@ -277,30 +312,31 @@ __device__ __forceinline__ void muon_update(const TensorDesc &T, int64_t e, cons
     store_p<PK, N>(T, e, p);
 }
 
-template <int PK>
-__global__ __launch_bounds__(kThreads, 2) void muon_update_kernel(StepArgs a, MuonArgs ma, int32_t from) {
-    __shared__ __align__(1024) char lds[2 * kStageBytes];
-    __shared__ Scalars S;
-    step_begin(a, S);
-    const StepCommit commit{a, S};
-    if (S.skip) return;
+template <int W, bool PAIR, int PK>
+__global__ __launch_bounds__((Tile<W, PAIR>::kLanes), (Tile<W, PAIR>::kWavesPerSimd)) void muon_update_kernel(StepArgs a, MuonArgs ma, int32_t from) {
+    __shared__ __align__(1024) char lds[Tile<W, PAIR>::kLds];
+    __shared__ Scalars sc;
+    step_begin(a, sc);
+    const StepCommit commit{a, sc};
+    if (sc.skip) return;
     const MuonTile t = ma.full[blockIdx.x];
+    if (t.mat < 0) return;
     const MuonMat M = ma.mats[t.mat];
     const char *X = ma.ws + M.x[from];
-    Sums s{};
-    apply_product(ma, t, M, X, lds, s);
+    Sums<W> s{};
+    apply_product<W, PAIR>(ma, t, M, X, lds_at(lds), s);
     const TensorDesc T = uniform_desc(a.tensors[M.tensor]);
     const double r = M.rows, c = M.cols;
     const double scale = ma.scale_kind == OPTIM_MUON_SCALE_RMS      ? 0.2 * sqrt(r > c ? r : c)
                          : ma.scale_kind == OPTIM_MUON_SCALE_ASPECT ? sqrt(r > c ? r / c : 1.0)
                                                                     : 1.0;
-    const float f = (float)(S.lr64 * scale), lw = S.lrwd[T.group];
+    const float f = (float)(sc.lr64 * scale), lw = sc.lrwd[T.group];
     const bool vec = T.vec_ok && (M.cols & 3) == 0 && (M.elem0 & 3) == 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < Tile<W, PAIR>::kOutJ; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int32_t rr = t.i * kTile + row0() + 16 * j, cc = t.j * kTile + col0() + 16 * i;
+            const int32_t rr = t.i * Tile<W>::kSide + row0<W, PAIR>() + 16 * j, cc = t.j * Tile<W>::kSide + col0<W>() + 16 * i;
             if (rr >= M.rows || cc >= M.cols) continue;
             float x[4];
             load_split4(X, split_at(rr, cc, M.ld), x);
@@ -316,9 +352,54 @@ __global__ __launch_bounds__(kThreads, 2) void muon_update_kernel(StepArgs a, Mu
 
 }  // namespace
 
-template <int PK>
-static void launch_update(const StepArgs &a, const MuonArgs &ma, int64_t grid, int32_t from, hipStream_t s) {
-    LAUNCH_TRACED((muon_update_kernel<PK>), (unsigned)grid, kThreads, s, a, ma, from);
+template <int W, bool PAIR>
+static void launch_gram(const StepArgs &a, const MuonArgs &ma, int64_t tiles, int32_t from, hipStream_t s) {
+    LAUNCH_TRACED((muon_gram_kernel<W, PAIR>), (unsigned)tiles, (Tile<W, PAIR>::kLanes), s, a, ma, from);
+}
+template <int W, bool PAIR>
+static void launch_square(const StepArgs &a, const MuonArgs &ma, int64_t tiles, hipStream_t s) {
+    LAUNCH_TRACED((muon_square_kernel<W, PAIR>), (unsigned)tiles, (Tile<W, PAIR>::kLanes), s, a, ma);
+}
+
+template <int W, bool PAIR, int PK>
+static void launch_update(const StepArgs &a, const MuonArgs &ma, int64_t tiles, int32_t from, hipStream_t s) {
+    LAUNCH_TRACED((muon_update_kernel<W, PAIR, PK>), (unsigned)tiles, (Tile<W, PAIR>::kLanes), s, a, ma, from);
+}
+// pk < 0: another iteration follows
+template <int W, bool PAIR>
+static void launch_apply(const StepArgs &a, const MuonArgs &ma, int64_t tiles, int32_t from, int pk, hipStream_t s) {
+    if (pk < 0)
+        LAUNCH_TRACED((muon_apply_kernel<W, PAIR>), (unsigned)tiles, (Tile<W, PAIR>::kLanes), s, a, ma, from);
+    else if (pk == P_F32)
+        launch_update<W, PAIR, P_F32>(a, ma, tiles, from, s);
+    else if (pk == P_BF16R)
+        launch_update<W, PAIR, P_BF16R>(a, ma, tiles, from, s);
+    else if (pk == P_MBF16)
+        launch_update<W, PAIR, P_MBF16>(a, ma, tiles, from, s);
+    else
+        launch_update<W, PAIR, P_MF16>(a, ma, tiles, from, s);
+}
+
+// One iteration over the tiles of a run: the wide ones, then the others.
+static void launch_iteration(const StepArgs &a, const MuonArgs &args, const MuonRun &R, int32_t from, int pk,
+                             bool commit, hipStream_t s) {
+    MuonArgs ma = args, rest = args;
+    ma.sym += R.sym0;
+    ma.full += R.full0;
+    rest.sym = ma.sym + R.wide_sym;
+    rest.full = ma.full + R.wide_full;
+    if (R.wide_sym) launch_gram<2, false>(a, ma, R.wide_sym, from, s);
+    if (R.nsym && R.pair_sym) launch_gram<1, true>(a, rest, R.nsym, from, s);
+    else if (R.nsym) launch_gram<1, false>(a, rest, R.nsym, from, s);
+    if (R.wide_sym) launch_square<2, false>(a, ma, R.wide_sym, s);
+    if (R.nsym && R.pair_sym) launch_square<1, true>(a, rest, R.nsym, s);
+    else if (R.nsym) launch_square<1, false>(a, rest, R.nsym, s);
+    StepArgs b = a;
+    b.commit = commit && !R.nfull;  // the last launch publishes the step
+    if (R.wide_full) launch_apply<2, false>(b, ma, R.wide_full, from, pk, s);
+    b.commit = commit;
+    if (R.nfull && R.pair_full) launch_apply<1, true>(b, rest, R.nfull, from, pk, s);
+    else if (R.nfull) launch_apply<1, false>(b, rest, R.nfull, from, pk, s);
 }
 
 hipError_t launch_muon(const StepArgs &args, const MuonArgs &margs, int pk, int gk, int32_t steps, int32_t nesterov,
@@ -337,26 +418,13 @@ hipError_t launch_muon(const StepArgs &args, const MuonArgs &margs, int pk, int 
         MuonArgs ma = margs;
         ma.mat0 = R.mat0;
         ma.mat1 = R.mat1;
-        ma.sym += R.sym0;
-        ma.full += R.full0;
         if (gk == G_F32)
             LAUNCH_TRACED((muon_split_kernel<G_F32>), (unsigned)R.units, kThreads, s, a, ma, nesterov);
         else
             LAUNCH_TRACED((muon_split_kernel<G_BF16>), (unsigned)R.units, kThreads, s, a, ma, nesterov);
         for (int32_t i = 0; i < steps; ++i) {
-            const int32_t from = i & 1;
-            LAUNCH_TRACED(muon_gram_kernel, (unsigned)R.nsym, kThreads, s, a, ma, from);
-            LAUNCH_TRACED(muon_square_kernel, (unsigned)R.nsym, kThreads, s, a, ma);
-            if (i + 1 < steps) {
-                LAUNCH_TRACED(muon_apply_kernel, (unsigned)R.nfull, kThreads, s, a, ma, from);
-                continue;
-            }
-            StepArgs b = a;
-            b.commit = k + 1 == nruns;
-            if (pk == P_F32) launch_update<P_F32>(b, ma, R.nfull, from, s);
-            else if (pk == P_BF16R) launch_update<P_BF16R>(b, ma, R.nfull, from, s);
-            else if (pk == P_MBF16) launch_update<P_MBF16>(b, ma, R.nfull, from, s);
-            else launch_update<P_MF16>(b, ma, R.nfull, from, s);
+            const bool last = i + 1 == steps;
+            launch_iteration(a, ma, R, i & 1, last ? pk : -1, last && k + 1 == nruns, s);
         }
         e = hipGetLastError();
     }

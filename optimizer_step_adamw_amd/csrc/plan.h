@@ -206,8 +206,9 @@ static_assert(sizeof(GradItem) == 24, "GradItem layout");
 // Muon: a matrix of the list with its arrays in the workspace (byte offsets
 // from the region that the runs share).  X is held padded to rp x ld, A and B
 // to sp x sp, sides rounded up to whole product tiles.
-constexpr int kMuonTile = 128;
+constexpr int kMuonTile = 128, kMuonWideTile = 256;
 constexpr int64_t kMuonUnit = 4096;  // elements of padded X per workgroup of the splitting pass
+constexpr int64_t kMuonWideMin = 512;  // shorter side of matrices that may take wide tiles
 constexpr int64_t kMuonMaxSide = int64_t(1) << 20;
 constexpr int64_t kMuonRunBytes = int64_t(4) << 30;  // workspace of one run of launches
 struct MuonMat {          // 80 bytes
@@ -227,11 +228,17 @@ struct MuonTile {         // 8 bytes
     uint16_t i, j;        // tile row and column
 };
 static_assert(sizeof(MuonTile) == 8, "MuonTile layout");
+// Compute units of the GPU that tiles are dealt out to.
+constexpr int64_t kMuonSlots = 256;
 struct MuonRun {          // matrices [mat0, mat1) that share a run of launches
     int32_t mat0, mat1;
     int64_t units;        // of the splitting pass
-    int64_t sym0, nsym;   // tiles of the symmetric products
-    int64_t full0, nfull; // tiles of X
+    // tiles of the symmetric products, and of X: wide ones, then others
+    int64_t sym0, wide_sym, nsym;
+    int64_t full0, wide_full, nfull;
+    int32_t wide;         // matrices padded to kMuonWideTile, else kMuonTile
+    int32_t pair_sym, pair_full;  // the others by two groups of wavefronts each
+    int32_t pad_;
 };
 
 // Workspace layout (byte offsets from the workspace base, 256-aligned).
