@@ -135,7 +135,10 @@ struct Built {
     std::vector<MuonTile> sym, full;
     std::vector<MuonRun> runs;
     int64_t muon_bytes = 0;         // of the region the runs share
-    int64_t muon_tiles = 0;
+    int64_t muon_tiles = 0, muon_end = 0;
+    int run_kind = -1;
+    int32_t lone0 = -1, lone_narrow = 0;  // matrices of one slab
+    int64_t lone_unit0 = 0;
     Layout L{};
 };
 
@@ -262,11 +265,18 @@ void add_product(const Built &B, const MuonRun &R, bool upper, std::vector<MuonT
 void add_tiles(Built &B) {
     int64_t sym = 0, full = 0;
     for (const MuonMat &M : B.mats) {
+        if (M.slabs) continue;
         const int64_t nt = M.sp / kMuonTile;
         sym += nt * (nt + 1) / 2;
         full += (int64_t)(M.rp / kMuonTile) * (M.ld / kMuonTile);
     }
     for (MuonRun &R : B.runs) {
+        if (R.slabs) {
+            R.full0 = (int64_t)B.full.size();
+            for (int32_t m = R.mat0; m < R.mat1; ++m)
+                for (int32_t k = 0; k < B.mats[m].slabs; ++k) B.full.push_back(MuonTile{m, (uint16_t)k, 0});
+            continue;
+        }
         add_product(B, R, true, B.sym, R.sym0, R.wide_sym, R.nsym);
         add_product(B, R, false, B.full, R.full0, R.wide_full, R.nfull);
         R.pair_sym = sym <= kMuonSlots;
@@ -274,41 +284,61 @@ void add_tiles(Built &B) {
     }
 }
 
-// Muon: the matrices of tensor i and their arrays.  A run takes
-// matrices until their arrays pass `cap` bytes.
-int add_matrices(const std::string &ti, int i, int64_t numel, int64_t rows, int64_t cols, bool wide, int64_t cap,
+// How a matrix is multiplied: by wide tiles, by tiles, through several slabs or
+// through one, of a short side padded to 64 or 128.
+enum MuonKind { kWide = 0, kTiles, kSlabs64, kSlabs128, kLone64, kLone128, kMuonKinds };
+
+int64_t muon_slabs(int64_t rows, int64_t cols) {
+    const int64_t sp = std::min(rows, cols) <= 64 ? 64 : 128, l = kMuonSlab / sp;
+    return (std::max(rows, cols) + l - 1) / l;
+}
+
+MuonKind muon_kind(int64_t rows, int64_t cols, bool wide) {
+    const int64_t s = std::min(rows, cols), p = muon_slabs(rows, cols);
+    if (s <= 128 && p == 1) return s <= 64 ? kLone64 : kLone128;
+    if (s <= 128 && p <= kMuonMaxSlabs) return s <= 64 ? kSlabs64 : kSlabs128;
+    return wide && wide_matrix(rows, cols) ? kWide : kTiles;
+}
+
+// Muon: the matrices of tensor i and their arrays.  A run takes matrices of
+// one kind (slabs: of both) until their arrays pass `cap` bytes.
+int add_matrices(const std::string &ti, int i, int64_t numel, int64_t rows, int64_t cols, MuonKind kind, int64_t cap,
                  Built &B) {
-    if (rows < 1 || cols < 1 || rows > kMuonMaxSide || cols > kMuonMaxSide)
-        return fail(OPTIM_EINVAL, ti + "rows and cols must be in [1, 2^20]");
     if (numel % (rows * cols) != 0) return fail(OPTIM_EINVAL, ti + "numel must be a multiple of rows * cols");
     const int64_t count = numel / (rows * cols);
-    const int64_t tile = wide ? kMuonWideTile : kMuonTile;
-    const int64_t rp = round_up(rows, tile), ld = round_up(cols, tile), sp = std::min(rp, ld);
-    const int64_t bytes = 2 * (rp * ld * 4) + 2 * (sp * sp * 4);
+    const bool slabs = kind >= kSlabs64, lone = kind >= kLone64;
+    const int run_kind = slabs ? kSlabs64 : kind;
+    const int64_t tile = kind == kWide ? kMuonWideTile : kMuonTile;
+    const int64_t rp = round_up(rows, tile), ld = round_up(cols, tile);
+    const int64_t sp = !slabs ? std::min(rp, ld) : kind == kSlabs64 || kind == kLone64 ? 64 : 128;
+    const int64_t p = slabs ? muon_slabs(rows, cols) : 0;
+    // X twice (slabs: once, in place), A and B (slabs: two sets of parts of A)
+    const int64_t xbytes = lone ? 0 : slabs ? p * kMuonSlab * 4 : rp * ld * 4;
+    const int64_t abytes = lone ? 0 : slabs ? p * sp * sp * 4 : sp * sp * 4;
+    const int64_t bytes = (slabs ? 1 : 2) * xbytes + 2 * abytes;
     const int64_t nt = sp / tile;
-    const int64_t tiles = nt * (nt + 1) / 2 + (rp / tile) * (ld / tile);
-    if (count > INT32_MAX / 4 || (int64_t)B.mats.size() + count > INT32_MAX / 4 ||
+    const int64_t tiles = slabs ? p : nt * (nt + 1) / 2 + (rp / tile) * (ld / tile);
+    if (count > INT32_MAX / 4 || (int64_t)B.mats.size() + count > ((int64_t)1 << 26) ||
         tiles > (((int64_t)1 << 26) - B.muon_tiles) / count)
         return fail(OPTIM_EUNSUPPORTED, ti + "too many matrices or tiles");
     B.muon_tiles += tiles * count;
     for (int64_t k = 0; k < count; ++k) {
-        int64_t used = B.mats.empty() ? 0 : B.mats.back().b + (int64_t)B.mats.back().sp * B.mats.back().sp * 4;
-        if (B.runs.empty() || B.runs.back().wide != (int32_t)wide || used + bytes > cap) {
+        int64_t used = B.muon_end;
+        if (!lone && (B.runs.empty() || B.run_kind != run_kind || used + bytes > cap)) {
             const int32_t m = (int32_t)B.mats.size();
             MuonRun R{};
             R.mat0 = R.mat1 = m;
-            R.wide = wide;
+            R.wide = kind == kWide;
             B.runs.push_back(R);
+            B.run_kind = run_kind;
             used = 0;
         }
-        MuonRun &R = B.runs.back();
         MuonMat M{};
         M.elem0 = k * rows * cols;
         M.x[0] = used;
-        M.x[1] = M.x[0] + rp * ld * 4;
-        M.a = M.x[1] + rp * ld * 4;
-        M.b = M.a + sp * sp * 4;
-        M.unit0 = R.units;
+        M.x[1] = M.x[0] + (slabs ? 0 : xbytes);
+        M.a = M.x[1] + xbytes;
+        M.b = M.a + abytes;
         M.tensor = i;
         M.rows = (int32_t)rows;
         M.cols = (int32_t)cols;
@@ -316,17 +346,63 @@ int add_matrices(const std::string &ti, int i, int64_t numel, int64_t rows, int6
         M.rp = (int32_t)rp;
         M.sp = (int32_t)sp;
         M.tall = rows > cols;
+        M.slabs = (int32_t)p;
         const int32_t m = (int32_t)B.mats.size();
+        if (!lone) {
+            MuonRun &R = B.runs.back();
+            M.unit0 = R.units;
+            R.mat1 = m + 1;
+            if (slabs) {
+                R.slabs += p;
+                if (sp == 64) R.narrow += p;
+            } else {
+                R.units += rp * ld / kMuonUnit;
+            }
+            B.muon_end = used + bytes;
+            B.muon_bytes = std::max(B.muon_bytes, B.muon_end);
+        } else if (B.lone0 < 0) {
+            B.lone0 = m;
+            B.lone_unit0 = B.nunits;
+        }
+        if (kind == kLone64) ++B.lone_narrow;
         B.mats.push_back(M);
-        R.mat1 = m + 1;
-        R.units += rp * ld / kMuonUnit;
-        B.muon_bytes = std::max(B.muon_bytes, used + bytes);
         // a span per matrix: its units' sums of squares give its norm
         B.blockspan.push_back((int32_t)B.spans.size());
         B.spans.push_back(SpanDesc{B.nunits, M.elem0, rows * cols, i, B.nblocks});
         B.nunits += (rows * cols + B.tile - 1) / B.tile;
         ++B.nblocks;
     }
+    return OPTIM_OK;
+}
+
+// Muon: the matrices of the list, kind by kind, so that a run's are of one
+// kind; wide tiles where all matrices that may take them make a round of the
+// GPU.
+int add_muon(const optim_tensor_list *list, int64_t cap, Built &B) {
+    int64_t wide_full = 0;
+    for (int i = 0; i < list->n; ++i) {
+        if (list->numel[i] == 0) continue;
+        const int64_t r = list->rows[i], c = list->cols[i];
+        if (r < 1 || c < 1 || r > kMuonMaxSide || c > kMuonMaxSide)
+            return fail(OPTIM_EINVAL, "tensor " + std::to_string(i) + ": rows and cols must be in [1, 2^20]");
+        if (muon_kind(r, c, true) == kWide)
+            wide_full += list->numel[i] / (r * c) * (round_up(r, kMuonWideTile) / kMuonWideTile) *
+                         (round_up(c, kMuonWideTile) / kMuonWideTile);
+    }
+    for (int kind = 0; kind < kMuonKinds; ++kind)
+        for (int i = 0; i < list->n; ++i) {
+            if (list->numel[i] == 0) continue;
+            const int64_t r = list->rows[i], c = list->cols[i];
+            if (muon_kind(r, c, wide_full >= kMuonSlots) != kind) continue;
+            if (const int rc = add_matrices("tensor " + std::to_string(i) + ": ", i, list->numel[i], r, c, (MuonKind)kind,
+                                            cap, B))
+                return rc;
+        }
+    if (B.lone0 < 0) {
+        B.lone0 = (int32_t)B.mats.size();
+        B.lone_unit0 = B.nunits;
+    }
+    add_tiles(B);
     return OPTIM_OK;
 }
 
@@ -739,26 +815,8 @@ int build(const optim_tensor_list *list, int32_t algo, const optim_plan_opts *op
             }
         }
     }
-    // Muon: wide tiles where all matrices that may take them make a round of
-    // the GPU; these matrices first, then the others, so that a run's matrices
-    // are of one kind
-    int64_t wide_full = 0;
-    for (int i = 0; muon && i < n; ++i) {
-        const int64_t r = list->rows[i], c = list->cols[i];
-        if (list->numel[i] > 0 && r > 0 && c > 0 && r <= kMuonMaxSide && c <= kMuonMaxSide && wide_matrix(r, c))
-            wide_full += list->numel[i] / (r * c) * (round_up(r, kMuonWideTile) / kMuonWideTile) *
-                         (round_up(c, kMuonWideTile) / kMuonWideTile);
-    }
-    for (int pass = 0; muon && pass < 2; ++pass)
-        for (int i = 0; i < n; ++i) {
-            if (list->numel[i] == 0) continue;
-            const int64_t r = list->rows[i], c = list->cols[i];
-            const bool wide = wide_full >= kMuonSlots && wide_matrix(r, c);
-            if (wide != (pass == 0)) continue;
-            if (const int rc = add_matrices("tensor " + std::to_string(i) + ": ", i, list->numel[i], r, c, wide, seg_cap, B))
-                return rc;
-        }
-    add_tiles(B);
+    if (muon)
+        if (const int rc = add_muon(list, seg_cap, B)) return rc;
     close_pack();
     B.pack_unit0 = B.nunits;
     for (size_t k = 0; k < B.packs.size(); ++k) {
@@ -822,6 +880,8 @@ struct optim_plan {
     Layout L;
     std::vector<MiniSegment> segs;  // Adam-mini launch segments
     std::vector<MuonRun> runs;      // Muon: runs of launches
+    int32_t lone0, lone_narrow;     // Muon: matrices of one slab (MuonArgs)
+    int64_t lone_unit0;
     int32_t interleaved;            // blockwise: interleaved state layout
     int32_t sched;
     double lr_max, lr_min;
@@ -985,6 +1045,9 @@ int create_on(const Built &B, const optim_tensor_list *list, int32_t algo, const
     P->L = B.L;
     P->segs = B.segs;
     P->runs = B.runs;
+    P->lone0 = B.lone0;
+    P->lone_narrow = B.lone_narrow;
+    P->lone_unit0 = B.lone_unit0;
     P->interleaved = B.interleaved ? 1 : 0;
     P->sched = OPTIM_SCHED_NONE;
     P->static_dev = dev;
@@ -1389,6 +1452,10 @@ int optim_step_muon(optim_plan *plan, const optim_muon_hp *hp, float *lr_dev, co
     ma.qb = (float)hp->b;
     ma.qc = (float)hp->c;
     ma.scale_kind = hp->scale_kind;
+    ma.lone0 = plan->lone0;
+    ma.lone_narrow = plan->lone_narrow;
+    ma.lone_unit0 = plan->lone_unit0;
+    ma.nmats = plan->nblocks;
     const TraceScope ts(plan);
     HIP_OK(launch_muon(a, ma, plan->pk, plan->gk, hp->steps, hp->nesterov != 0, plan->runs.data(),
                        (int32_t)plan->runs.size(), static_cast<hipStream_t>(stream)));

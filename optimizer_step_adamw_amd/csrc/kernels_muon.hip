@@ -11,29 +11,12 @@
 // A and B are symmetric: only tiles on and above the diagonal are computed
 // and each is stored on both sides.
 // One launch of a kernel covers the tiles of every matrix of a run, from a
-// table of (matrix, tile row, tile column).
-#include "optim_muon.h"
-
-#include "tiles.h"
+// table of (matrix, tile row, tile column).  Matrices with a side of at most
+// 128 go another way (kernels_muon_slab.hip).
+#include "muon_common.h"
 
 namespace optim {
 namespace {
-
-// X, A and B are stored times 2^12: bounded by 15 (checked on the host) they
-// stay below fp16's 65504, and a typical element of a 4096 x 4096 X, 2^-12 at
-// the start and 2^-6 at the end, has both its parts well above fp16's
-// smallest subnormal, 2^-24.
-constexpr float kMuonScale = 4096.0f, kMuonUnscale = 1.0f / 4096.0f;
-
-__device__ __forceinline__ bool skipped(const StepArgs &a) {
-    return a.prep.found_inf && *a.prep.found_inf != 0.0f;
-}
-
-template <int N>
-__device__ __forceinline__ void muon_u(const float (&g)[N], float (&m)[N], float mu, bool nesterov, float (&u)[N]) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) u[i] = nesterov ? g[i] + mu * m[i] : m[i];
-}
 
 // ---------------------------------------------------------------- momentum
 // m <- mu m + g and each unit's sum of u^2 (fp64: a square overflows fp32
@@ -70,12 +53,11 @@ __global__ __launch_bounds__(kThreads) void muon_momentum_kernel(StepArgs a, int
     });
 }
 
-// Per matrix, the factor kMuonScale / (||u|| + eps), in fp64 (with eps 0 and
-// a small u it may leave fp32's range; the scaled u does not).
-__global__ __launch_bounds__(kThreads) void muon_norm_kernel(StepArgs a) {
+// Per matrix, the factor that normalises it.
+__global__ __launch_bounds__(kThreads) void muon_norm_kernel(StepArgs a, int32_t mats) {
     if (skipped(a)) return;
     __shared__ double red[kThreads];
-    for (int b = blockIdx.x; b < a.nblocks; b += gridDim.x) {
+    for (int b = blockIdx.x; b < mats; b += gridDim.x) {
         const int si = a.blockspan[b];
         red[threadIdx.x] = lane_sum(a.partials, 1, a.spans[si].unit_begin, a.spans[si + 1].unit_begin);
         __syncthreads();
@@ -84,8 +66,7 @@ __global__ __launch_bounds__(kThreads) void muon_norm_kernel(StepArgs a) {
             __syncthreads();
         }
         if (threadIdx.x == 0) {
-            const double n = sqrt(red[0]) + a.prep.eps;
-            reinterpret_cast<double *>(a.blockfac)[b] = n == 0.0 ? 0.0 : (double)kMuonScale / n;
+            reinterpret_cast<double *>(a.blockfac)[b] = muon_factor(red[0], a.prep.eps);
         }
         __syncthreads();
     }
@@ -102,18 +83,6 @@ __device__ __forceinline__ int muon_find(const MuonArgs &a, int64_t u) {
 }
 
 // Four values of a split array as two 8-byte stores.
-__device__ __forceinline__ void split4(const float (&x)[4], uint2 &hi, uint2 &lo) {
-    f16x4 h, l;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        _Float16 a, b;
-        split2(x[i], a, b);
-        h[i] = a;
-        l[i] = b;
-    }
-    hi = __builtin_bit_cast(uint2, h);
-    lo = __builtin_bit_cast(uint2, l);
-}
 __device__ __forceinline__ void put_split4(char *base, int64_t at, uint2 hi, uint2 lo) {
     GMEM u32x2 *q = (GMEM u32x2 *)gp(base + at * 2);
     q[0] = u32x2{hi.x, hi.y};
@@ -302,16 +271,6 @@ __global__ __launch_bounds__((Tile<W, PAIR>::kLanes), (Tile<W, PAIR>::kWavesPerS
         }
 }
 
-// The last application and the update.
-template <int PK, int N>
-__device__ __forceinline__ void muon_update(const TensorDesc &T, int64_t e, const float *x, float lw, float f) {
-    float p[N];
-    load_p<PK, N>(T, e, p);
-#pragma unroll
-    for (int i = 0; i < N; ++i) p[i] = decayed(p[i], lw, f * x[i]);
-    store_p<PK, N>(T, e, p);
-}
-
 template <int W, bool PAIR, int PK>
 __global__ __launch_bounds__((Tile<W, PAIR>::kLanes), (Tile<W, PAIR>::kWavesPerSimd)) void muon_update_kernel(StepArgs a, MuonArgs ma, int32_t from) {
     __shared__ __align__(1024) char lds[Tile<W, PAIR>::kLds];
@@ -326,10 +285,7 @@ __global__ __launch_bounds__((Tile<W, PAIR>::kLanes), (Tile<W, PAIR>::kWavesPerS
     Sums<W> s{};
     apply_product<W, PAIR>(ma, t, M, X, lds_at(lds), s);
     const TensorDesc T = uniform_desc(a.tensors[M.tensor]);
-    const double r = M.rows, c = M.cols;
-    const double scale = ma.scale_kind == OPTIM_MUON_SCALE_RMS      ? 0.2 * sqrt(r > c ? r : c)
-                         : ma.scale_kind == OPTIM_MUON_SCALE_ASPECT ? sqrt(r > c ? r / c : 1.0)
-                                                                    : 1.0;
+    const double scale = muon_scale(ma.scale_kind, M.rows, M.cols);
     const float f = (float)(sc.lr64 * scale), lw = sc.lrwd[T.group];
     const bool vec = T.vec_ok && (M.cols & 3) == 0 && (M.elem0 & 3) == 0;
 #pragma unroll
@@ -404,30 +360,40 @@ static void launch_iteration(const StepArgs &a, const MuonArgs &args, const Muon
 
 hipError_t launch_muon(const StepArgs &args, const MuonArgs &margs, int pk, int gk, int32_t steps, int32_t nesterov,
                        const MuonRun *runs, int32_t nruns, hipStream_t s) {
+    // matrices that one workgroup each takes through the whole step
+    const int64_t lone = margs.nmats - margs.lone0;
     StepArgs a = args;
-    a.commit = nruns == 0;  // else the last update publishes the step
-    if (gk == G_F32)
-        LAUNCH_TRACED((muon_momentum_kernel<G_F32>), persistent_grid(0, a), kThreads, s, a, nesterov);
-    else
-        LAUNCH_TRACED((muon_momentum_kernel<G_BF16>), persistent_grid(0, a), kThreads, s, a, nesterov);
+    a.commit = nruns == 0 && lone == 0;  // else the last launch publishes the step
+    a.nunits = margs.lone_unit0;
+    if (nruns > 0 || lone == 0) {
+        if (gk == G_F32)
+            LAUNCH_TRACED((muon_momentum_kernel<G_F32>), persistent_grid(0, a), kThreads, s, a, nesterov);
+        else
+            LAUNCH_TRACED((muon_momentum_kernel<G_BF16>), persistent_grid(0, a), kThreads, s, a, nesterov);
+    }
     if (nruns > 0)
-        LAUNCH_TRACED(muon_norm_kernel, (unsigned)(a.nblocks < 2048 ? a.nblocks : 2048), kThreads, s, a);
+        LAUNCH_TRACED(muon_norm_kernel, (unsigned)(margs.lone0 < 2048 ? margs.lone0 : 2048), kThreads, s, a, margs.lone0);
     hipError_t e = hipGetLastError();
     for (int32_t k = 0; k < nruns && e == hipSuccess; ++k) {
         const MuonRun &R = runs[k];
         MuonArgs ma = margs;
         ma.mat0 = R.mat0;
         ma.mat1 = R.mat1;
+        if (R.slabs > 0) {
+            e = launch_muon_slabs(a, ma, R, pk, gk, steps, nesterov, lone == 0 && k + 1 == nruns, s);
+            continue;
+        }
         if (gk == G_F32)
             LAUNCH_TRACED((muon_split_kernel<G_F32>), (unsigned)R.units, kThreads, s, a, ma, nesterov);
         else
             LAUNCH_TRACED((muon_split_kernel<G_BF16>), (unsigned)R.units, kThreads, s, a, ma, nesterov);
         for (int32_t i = 0; i < steps; ++i) {
             const bool last = i + 1 == steps;
-            launch_iteration(a, ma, R, i & 1, last ? pk : -1, last && k + 1 == nruns, s);
+            launch_iteration(a, ma, R, i & 1, last ? pk : -1, last && lone == 0 && k + 1 == nruns, s);
         }
         e = hipGetLastError();
     }
+    if (e == hipSuccess && lone > 0) e = launch_muon_lone(args, margs, pk, gk, steps, nesterov, s);
     return e;
 }
 

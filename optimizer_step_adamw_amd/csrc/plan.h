@@ -208,6 +208,13 @@ static_assert(sizeof(GradItem) == 24, "GradItem layout");
 // to sp x sp, sides rounded up to whole product tiles.
 constexpr int kMuonTile = 128, kMuonWideTile = 256;
 constexpr int64_t kMuonUnit = 4096;  // elements of padded X per workgroup of the splitting pass
+// Matrices with a side of at most 128 go through slabs: kMuonSlab values of X
+// (positions along the longer side times the shorter side padded to 64 or 128)
+// that a workgroup holds in LDS.  A matrix of one slab has its whole step in
+// one launch; of several (up to kMuonMaxSlabs), their parts of A pass
+// through the workspace.
+constexpr int32_t kMuonSlab = 16384;
+constexpr int64_t kMuonMaxSlabs = 128;
 constexpr int64_t kMuonWideMin = 512;  // shorter side of matrices that may take wide tiles
 constexpr int64_t kMuonMaxSide = int64_t(1) << 20;
 constexpr int64_t kMuonRunBytes = int64_t(4) << 30;  // workspace of one run of launches
@@ -220,7 +227,7 @@ struct MuonMat {          // 80 bytes
     int32_t ld, rp;       // padded columns and rows of X
     int32_t sp;           // padded shorter side
     int32_t tall;         // rows > cols
-    int32_t pad_;
+    int32_t slabs;        // of a matrix with a short side (sp 64 or 128)
 };
 static_assert(sizeof(MuonMat) == 80, "MuonMat layout");
 struct MuonTile {         // 8 bytes
@@ -236,6 +243,9 @@ struct MuonRun {          // matrices [mat0, mat1) that share a run of launches
     // tiles of the symmetric products, and of X: wide ones, then others
     int64_t sym0, wide_sym, nsym;
     int64_t full0, wide_full, nfull;
+    // slabs of matrices of a short side of at most 64 (then 128): of `slabs`
+    // in the table from full0 on, the first `narrow`; 0: products by tiles
+    int64_t slabs, narrow;
     int32_t wide;         // matrices padded to kMuonWideTile, else kMuonTile
     int32_t pair_sym, pair_full;  // the others by two groups of wavefronts each
     int32_t pad_;
@@ -381,7 +391,15 @@ struct MuonArgs {
     int32_t mat0, mat1;   // this run's matrices
     float qa, qb, qc;     // the quintic
     int32_t scale_kind;
+    // matrices of one slab: [lone0, nmats), the first lone_narrow of them of
+    // sp 64; units from lone_unit0 on
+    int32_t lone0, lone_narrow, nmats;
+    int64_t lone_unit0;
 };
+hipError_t launch_muon_slabs(const StepArgs &a, const MuonArgs &ma, const MuonRun &R, int pk, int gk, int32_t steps,
+                             int32_t nesterov, bool commit, hipStream_t s);
+hipError_t launch_muon_lone(const StepArgs &a, const MuonArgs &ma, int pk, int gk, int32_t steps, int32_t nesterov,
+                            hipStream_t s);
 hipError_t launch_muon(const StepArgs &a, const MuonArgs &ma, int pk, int gk, int32_t steps, int32_t nesterov,
                        const MuonRun *runs, int32_t nruns, hipStream_t s);
 

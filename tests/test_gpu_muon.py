@@ -25,9 +25,10 @@ pytestmark = pytest.mark.gpu
 
 TOL_DIRECTION = 900 * 2.0 ** -22
 COEF = (3.4445, -4.7750, 2.0315)
-# sides of one, both sides of a tile, tall and wide, stacks, odd columns
+# sides of one, both sides of a tile and of a slab, tall and wide, stacks, odd columns
 SHAPES = [(1, 1, 1), (1, 1, 7), (1, 5, 1), (2, 3, 5), (1, 64, 64), (1, 172, 64), (1, 64, 172), (1, 128, 128),
-          (1, 129, 127), (1, 127, 129), (1, 130, 300), (1, 300, 131), (3, 40, 72), (2, 257, 33), (1, 1000, 408), (1, 96, 2000)]
+          (1, 129, 127), (1, 127, 129), (1, 130, 300), (1, 300, 131), (3, 40, 72), (2, 257, 33), (1, 1000, 408), (1, 96, 2000),
+          (2, 64, 257), (1, 256, 64), (1, 65, 128), (2, 65, 130), (1, 1025, 17), (1, 1, 3000)]
 
 
 def direction64(u, coef=COEF, steps=5, eps=1e-7):
