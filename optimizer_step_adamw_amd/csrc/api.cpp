@@ -176,7 +176,8 @@ int check_hp_beta(double b, const char *name) {
 
 bool is_blockwise(int32_t algo) { return algo == OPTIM_ALGO_BLOCKWISE || algo == OPTIM_ALGO_BLOCKWISE_ADEMAMIX; }
 
-int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+int64_t count_of(int64_t n, int64_t of) { return (n + of - 1) / of; }
+int64_t round_up(int64_t n, int64_t to) { return count_of(n, to) * to; }
 // Whether a matrix may take wide tiles (in a plan with enough of them): below,
 // padding to whole wide tiles costs more than they gain.
 bool wide_matrix(int64_t rows, int64_t cols) { return std::min(rows, cols) >= kMuonWideMin; }
@@ -230,7 +231,7 @@ void add_product(const Built &B, const MuonRun &R, bool upper, std::vector<MuonT
     int64_t block = 0;
     for (int32_t m = R.mat0; m < R.mat1; ++m) {
         const MuonMat &M = B.mats[m];
-        const int64_t rows = (upper ? M.sp : M.rp) / tile, cols = (upper ? M.sp : M.ld) / tile;
+        const int64_t rows = count_of(upper ? M.sp : M.rp, tile), cols = count_of(upper ? M.sp : M.ld, tile);
         for (int64_t a = 0; a < rows; a += 4)
             for (int64_t b = upper ? a : 0; b < cols; b += 4, ++block)
                 for (int64_t i = a; i < std::min(a + 4, rows); ++i)
@@ -245,9 +246,11 @@ void add_product(const Built &B, const MuonRun &R, bool upper, std::vector<MuonT
         if (over <= kMuonSlots / 2) {
             for (size_t k = tiles.size() - over; k < tiles.size(); ++k) {
                 const MuonTile t = tiles[k].second;
+                const MuonMat &M = B.mats[t.mat];
                 for (int i = 0; i < 2; ++i)
                     for (int j = upper && t.i == t.j ? i : 0; j < 2; ++j)
-                        rest.push_back({tiles[k].first, MuonTile{t.mat, (uint16_t)(2 * t.i + i), (uint16_t)(2 * t.j + j)}});
+                        if ((2 * t.i + i) * kMuonTile < (upper ? M.sp : M.rp) && (2 * t.j + j) * kMuonTile < (upper ? M.sp : M.ld))
+                            rest.push_back({tiles[k].first, MuonTile{t.mat, (uint16_t)(2 * t.i + i), (uint16_t)(2 * t.j + j)}});
             }
             tiles.resize(tiles.size() - over);
         }
@@ -266,9 +269,9 @@ void add_tiles(Built &B) {
     int64_t sym = 0, full = 0;
     for (const MuonMat &M : B.mats) {
         if (M.slabs) continue;
-        const int64_t nt = M.sp / kMuonTile;
+        const int64_t nt = count_of(M.sp, kMuonTile);
         sym += nt * (nt + 1) / 2;
-        full += (int64_t)(M.rp / kMuonTile) * (M.ld / kMuonTile);
+        full += count_of(M.rp, kMuonTile) * count_of(M.ld, kMuonTile);
     }
     for (MuonRun &R : B.runs) {
         if (R.slabs) {
@@ -309,15 +312,15 @@ int add_matrices(const std::string &ti, int i, int64_t numel, int64_t rows, int6
     const bool slabs = kind >= kSlabs64, lone = kind >= kLone64;
     const int run_kind = slabs ? kSlabs64 : kind;
     const int64_t tile = kind == kWide ? kMuonWideTile : kMuonTile;
-    const int64_t rp = round_up(rows, tile), ld = round_up(cols, tile);
+    const int64_t rp = round_up(rows, 32), ld = round_up(cols, 32);
     const int64_t sp = !slabs ? std::min(rp, ld) : kind == kSlabs64 || kind == kLone64 ? 64 : 128;
     const int64_t p = slabs ? muon_slabs(rows, cols) : 0;
     // X twice (slabs: once, in place), A and B (slabs: two sets of parts of A)
     const int64_t xbytes = lone ? 0 : slabs ? p * kMuonSlab * 4 : rp * ld * 4;
     const int64_t abytes = lone ? 0 : slabs ? p * sp * sp * 4 : sp * sp * 4;
     const int64_t bytes = (slabs ? 1 : 2) * xbytes + 2 * abytes;
-    const int64_t nt = sp / tile;
-    const int64_t tiles = slabs ? p : nt * (nt + 1) / 2 + (rp / tile) * (ld / tile);
+    const int64_t nt = count_of(sp, tile);
+    const int64_t tiles = slabs ? p : nt * (nt + 1) / 2 + count_of(rp, tile) * count_of(ld, tile);
     if (count > INT32_MAX / 4 || (int64_t)B.mats.size() + count > ((int64_t)1 << 26) ||
         tiles > (((int64_t)1 << 26) - B.muon_tiles) / count)
         return fail(OPTIM_EUNSUPPORTED, ti + "too many matrices or tiles");
@@ -354,9 +357,10 @@ int add_matrices(const std::string &ti, int i, int64_t numel, int64_t rows, int6
             R.mat1 = m + 1;
             if (slabs) {
                 R.slabs += p;
+                R.most_slabs = std::max(R.most_slabs, (int32_t)p);
                 if (sp == 64) R.narrow += p;
             } else {
-                R.units += rp * ld / kMuonUnit;
+                R.units += count_of(rp * ld, kMuonUnit);
             }
             B.muon_end = used + bytes;
             B.muon_bytes = std::max(B.muon_bytes, B.muon_end);
@@ -386,8 +390,7 @@ int add_muon(const optim_tensor_list *list, int64_t cap, Built &B) {
         if (r < 1 || c < 1 || r > kMuonMaxSide || c > kMuonMaxSide)
             return fail(OPTIM_EINVAL, "tensor " + std::to_string(i) + ": rows and cols must be in [1, 2^20]");
         if (muon_kind(r, c, true) == kWide)
-            wide_full += list->numel[i] / (r * c) * (round_up(r, kMuonWideTile) / kMuonWideTile) *
-                         (round_up(c, kMuonWideTile) / kMuonWideTile);
+            wide_full += list->numel[i] / (r * c) * count_of(r, kMuonWideTile) * count_of(c, kMuonWideTile);
     }
     for (int kind = 0; kind < kMuonKinds; ++kind)
         for (int i = 0; i < list->n; ++i) {

@@ -215,22 +215,22 @@ __device__ __forceinline__ void load_p(const D &T, int64_t e, float (&p)[N]) {
     }
 }
 
-template <int PK, int N, class D>
+template <int PK, int N, int LAY = kStrided, class D>
 __device__ __forceinline__ void store_p(const D &T, int64_t e, const float (&p)[N]) {
     if constexpr (PK == P_F32) {
-        stf<N>(static_cast<float *>(T.p), e, p);
+        stf<N, LAY>(static_cast<float *>(T.p), e, p);
     } else if constexpr (PK == P_BF16R) {
         uint32_t b[N], r[N];
 #pragma unroll
         for (int k = 0; k < N; ++k) rem_split(p[k], b[k], r[k]);
-        sth<N>(static_cast<uint16_t *>(T.p), e, b);
-        sth<N>(T.rem, e, r);
+        sth<N, LAY>(static_cast<uint16_t *>(T.p), e, b);
+        sth<N, LAY>(T.rem, e, r);
     } else {
-        stf<N>(T.master, e, p);
+        stf<N, LAY>(T.master, e, p);
         uint32_t c[N];
 #pragma unroll
         for (int k = 0; k < N; ++k) c[k] = PK == P_MBF16 ? f32_to_bf16_rne(p[k]) : f32_to_f16_rne(p[k]);
-        sth<N>(static_cast<uint16_t *>(T.p), e, c);
+        sth<N, LAY>(static_cast<uint16_t *>(T.p), e, c);
     }
 }
 

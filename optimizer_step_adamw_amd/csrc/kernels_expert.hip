@@ -60,50 +60,49 @@ __device__ __forceinline__ void write_chunks(const Chunks &r, char *lds) {
         *(LMEM s16x8 *)(lds + (wave<W>() * 4 + t) * 1024 + (threadIdx.x & 63) * 16) = r.v[t];
 }
 
+// Four neighbouring elements of dW, n of which exist; `vec`: they are one access.
 template <bool F32>
-__device__ __forceinline__ float dw_get(const char *p, int64_t e) {
-    if constexpr (F32) return gp(reinterpret_cast<const float *>(p))[e];
-    else return bf16_to_f32(gp(reinterpret_cast<const uint16_t *>(p))[e]);
-}
-template <bool F32>
-__device__ __forceinline__ void dw_put(char *p, int64_t e, float x) {
-    if constexpr (F32) gp(reinterpret_cast<float *>(p))[e] = x;
-    else gp(reinterpret_cast<uint16_t *>(p))[e] = (uint16_t)f32_to_bf16_rne(x);
-}
-
-// Up to 4 neighbouring elements of dW from x, scaled and accumulated.
-template <bool F32>
-__device__ __forceinline__ void dw_store(const ExpertArgs &a, int64_t e, int n, f32x4 x, float s) {
-    if (a.out_vec) {  // (n is 4: a row is a multiple of 4)
-        if constexpr (F32) {
-            GMEM f32x4 *q = (GMEM f32x4 *)gp(a.dw + e * 4);
-            f32x4 y = x * s;
-            if (a.accumulate) y = *q + y;
-            *q = y;
-        } else {
-            GMEM u32x2 *q = (GMEM u32x2 *)gp(a.dw + e * 2);
-            float y[4];
+__device__ __forceinline__ f32x4 dw_get(const char *dw, int64_t e, int n, bool vec) {
+    f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+    if constexpr (F32) {
+        if (vec) return *(const GMEM f32x4 *)gp(dw + e * 4);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] = x[i] * s;
-            if (a.accumulate) {
-                const u32x2 old = *q;
-                y[0] += bf16_to_f32(old.x & 0xFFFFu);
-                y[1] += bf16_to_f32(old.x >> 16);
-                y[2] += bf16_to_f32(old.y & 0xFFFFu);
-                y[3] += bf16_to_f32(old.y >> 16);
-            }
-            *q = u32x2{f32_to_bf16_rne(y[0]) | f32_to_bf16_rne(y[1]) << 16,
-                       f32_to_bf16_rne(y[2]) | f32_to_bf16_rne(y[3]) << 16};
+        for (int i = 0; i < 4; ++i)
+            if (i < n) x[i] = gp(reinterpret_cast<const float *>(dw))[e + i];
+    } else {
+        if (vec) {
+            const u32x2 u = *(const GMEM u32x2 *)gp(dw + e * 2);
+            return f32x4{bf16_to_f32(u.x & 0xFFFFu), bf16_to_f32(u.x >> 16), bf16_to_f32(u.y & 0xFFFFu),
+                         bf16_to_f32(u.y >> 16)};
         }
-        return;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) x[i] = bf16_to_f32(gp(reinterpret_cast<const uint16_t *>(dw))[e + i]);
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (i < n) {
-            float y = x[i] * s;
-            if (a.accumulate) y = dw_get<F32>(a.dw, e + i) + y;
-            dw_put<F32>(a.dw, e + i, y);
+    return x;
+}
+template <bool F32>
+__device__ __forceinline__ void dw_put(char *dw, int64_t e, int n, bool vec, f32x4 x) {
+    if constexpr (F32) {
+        if (vec) {
+            *(GMEM f32x4 *)gp(dw + e * 4) = x;
+            return;
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) gp(reinterpret_cast<float *>(dw))[e + i] = x[i];
+    } else {
+        uint32_t u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u[i] = f32_to_bf16_rne(x[i]);
+        if (vec) {
+            *(GMEM u32x2 *)gp(dw + e * 2) = u32x2{u[0] | u[1] << 16, u[2] | u[3] << 16};
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) gp(reinterpret_cast<uint16_t *>(dw))[e + i] = (uint16_t)u[i];
+    }
 }
 
 // The rows of expert e's run that piece `piece` sums: whole steps of 64 but
@@ -141,8 +140,8 @@ __global__ __launch_bounds__(Tile<W>::kLanes, Tile<W>::kWavesPerSimd) void exper
     int32_t done = 0;
     if constexpr (DIRECT) {
         const int steps = rows / kStepRows;
-        product<W, false, KR, KR, false, BF16>(feed<W, KR, false>(x, a.ldx, mleft / 8), kStepRows * a.ldx,
-                                     feed<W, KR, false>(y, a.ldy, nleft / 8), kStepRows * a.ldy, steps, lds_at(lds), s);
+        product<W, false, KR, KR, false, BF16>(feed<W, KR, false>(x, a.ldx, mleft), kStepRows * a.ldx,
+                                     feed<W, KR, false>(y, a.ldy, nleft), kStepRows * a.ldy, steps, lds_at(lds), s);
         done = steps * kStepRows;
     }
     if (done < rows) {
@@ -173,27 +172,49 @@ __global__ __launch_bounds__(Tile<W>::kLanes, Tile<W>::kWavesPerSimd) void exper
         }
     }
     const float sc = a.scale ? *a.scale : 1.0f;
+    // (a row's accesses before those of the row ahead of it: the compiler keeps
+    // loads and stores of dW in order, and one at a time they would take a
+    // memory latency each)
+    const int32_t c0 = tj * Tile<W>::kSide + col0<W>();
+    auto place = [&](int i, int j, int64_t &at) {  // elements that exist
+        const int32_t r = ti * Tile<W>::kSide + row0<W>() + 16 * j, c = c0 + 16 * i;
+        at = ((int64_t)e * a.m + r) * a.n + c;
+        return r < a.m && c < a.n ? (a.n - c < 4 ? a.n - c : 4) : 0;
+    };
+    if (a.parts) {
+        float *parts = a.parts + ((int64_t)piece * a.experts * a.m) * a.n;
 #pragma unroll
-    for (int j = 0; j < Tile<W>::kJ; ++j)
+        for (int j = 0; j < Tile<W>::kJ; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                int64_t at;
+                if (const int n = place(i, j, at))
+                    dw_put<true>(reinterpret_cast<char *>(parts), at, n, (a.n & 3) == 0, s.v[i][j]);
+            }
+        return;
+    }
+    f32x4 old[2][4];
+    auto get = [&](int j) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int32_t r = ti * Tile<W>::kSide + row0<W>() + 16 * j, c = tj * Tile<W>::kSide + col0<W>() + 16 * i;
-            if (r >= a.m || c >= a.n) continue;
-            const int32_t n = a.n - c < 4 ? a.n - c : 4;
-            const int64_t at = ((int64_t)e * a.m + r) * a.n + c;
-            if (a.parts) {
-                float *q = a.parts + ((int64_t)piece * a.experts * a.m) * a.n + at;
-                if ((a.n & 3) == 0) {
-                    *(GMEM f32x4 *)gp(q) = s.v[i][j];
-                } else {
+            int64_t at;
+            if (const int n = place(i, j, at)) old[j & 1][i] = dw_get<F32>(a.dw, at, n, a.out_vec);
+        }
+    };
+    if (a.accumulate) get(0);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (k < n) gp(q)[k] = s.v[i][j][k];
-                }
-            } else {
-                dw_store<F32>(a, at, n, s.v[i][j], sc);
+    for (int j = 0; j < Tile<W>::kJ; ++j) {
+        if (a.accumulate && j + 1 < Tile<W>::kJ) get(j + 1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            int64_t at;
+            if (const int n = place(i, j, at)) {
+                f32x4 x = s.v[i][j] * sc;
+                if (a.accumulate) x = old[j & 1][i] + x;
+                dw_put<F32>(a.dw, at, n, a.out_vec, x);
             }
         }
+    }
 }
 
 // The pieces' sums in their order.
@@ -214,7 +235,10 @@ __global__ __launch_bounds__(kThreads) void expert_join_kernel(ExpertArgs a) {
                     if (i < n) x[i] += gp(q)[i];
             }
         }
-        dw_store<F32>(a, e, n, x, sc);
+        x = x * sc;
+        const bool vec = a.out_vec;
+        if (a.accumulate) x = dw_get<F32>(a.dw, e, n, vec) + x;
+        dw_put<F32>(a.dw, e, n, vec, x);
     }
 }
 

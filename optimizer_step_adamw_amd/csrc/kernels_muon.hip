@@ -4,8 +4,8 @@
 // The momentum pass is elementwise and bound by HBM; the iteration is matrix
 // products and bound by the matrix cores.  A matrix X (scaled by kMuonScale, so
 // that fp16's exponents reach what matters) is kept as a split array (tiles.h),
-// rows and columns padded to whole tiles with zeros, which the products keep
-// zero.  Nothing is ever transposed in memory: where rows <= cols ("wide")
+// rows and columns padded to multiples of 32 with zeros, which the products
+// keep zero.  Nothing is ever transposed in memory: where rows <= cols ("wide")
 // A = X X^T and X <- aX + B X, else A = X^T X and X <- aX + X B; the operand
 // whose k runs down its rows goes through the LDS's transposing read.
 // A and B are symmetric: only tiles on and above the diagonal are computed
@@ -93,13 +93,6 @@ __device__ __forceinline__ void store_split4(char *base, int64_t at, const float
     split4(x, hi, lo);
     put_split4(base, at, hi, lo);
 }
-__device__ __forceinline__ void load_split4(const char *base, int64_t at, float (&x)[4]) {
-    const GMEM f16x4 *q = (const GMEM f16x4 *)gp(base + at * 2);
-    const f16x4 hi = q[0], lo = q[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = (float)hi[i] + (float)lo[i];
-}
-
 // The normalised direction of a run's matrices as split arrays, padding as
 // zeros: kMuonUnit elements of the padded matrix per workgroup.
 template <int GK>
@@ -114,6 +107,7 @@ __global__ __launch_bounds__(kThreads) void muon_split_kernel(StepArgs a, MuonAr
     int64_t at = ((int64_t)blockIdx.x - M.unit0) * kMuonUnit + threadIdx.x * 4;
 #pragma unroll
     for (int k = 0; k < (int)(kMuonUnit / kSub); ++k, at += kSub) {
+        if (at >= (int64_t)M.rp * M.ld) break;
         const int32_t r = (int32_t)(at / M.ld), c = (int32_t)(at % M.ld);
         float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         if (r < M.rows && c < M.cols) {
@@ -141,14 +135,15 @@ __global__ __launch_bounds__(kThreads) void muon_split_kernel(StepArgs a, MuonAr
 }
 
 // ---------------------------------------------------------------- products
-// The operand whose rows (columns) are those of tile row (column) t.
+// The operand whose rows (columns) are those of tile row (column) t of an
+// array of `rows` (`cols`).
 template <int W>
-__device__ __forceinline__ Feed row_feed(const char *base, int t, int64_t rows32) {
-    return feed<W, KC, true>(base + (int64_t)t * (Tile<W>::kSide / 32) * rows32, rows32);
+__device__ __forceinline__ Feed row_feed(const char *base, int t, int64_t rows32, int rows) {
+    return feed<W, KC, true>(base + (int64_t)t * (Tile<W>::kSide / 32) * rows32, rows32, rows - t * Tile<W>::kSide);
 }
 template <int W>
-__device__ __forceinline__ Feed column_feed(const char *base, int t, int64_t rows32) {
-    return feed<W, KR, true>(base + (int64_t)t * (Tile<W>::kSide / 32) * kSplitBlock, rows32);
+__device__ __forceinline__ Feed column_feed(const char *base, int t, int64_t rows32, int cols) {
+    return feed<W, KR, true>(base + (int64_t)t * (Tile<W>::kSide / 32) * kSplitBlock, rows32, cols - t * Tile<W>::kSide);
 }
 
 // Transposes a 4 x 4 block of 16-bit numbers held by 4 neighbouring lanes:
@@ -167,24 +162,46 @@ __device__ __forceinline__ uint2 transpose4(uint2 d) {
     return q & 2 ? make_uint2(take, keep) : make_uint2(keep, take);
 }
 
-// Stores this wavefront's sums, through value(), as part of tile (ti, tj) of
-// the symmetric array at `base`, and transposed as part of tile (tj, ti).
-template <int W, bool PAIR, class F>
-__device__ __forceinline__ void store_symmetric(char *base, int64_t ld, int ti, int tj, F &&value) {
+// Up to four neighbouring split values of a row, as they lie in memory.
+struct Split4 {
+    u32x2 hi, lo;
+};
+__device__ __forceinline__ Split4 get_split4(const char *base, int64_t at) {
+    const GMEM u32x2 *q = (const GMEM u32x2 *)gp(base + at * 2);
+    return Split4{q[0], q[8]};
+}
+__device__ __forceinline__ void values(const Split4 &s, float (&x)[4]) {
+    const f16x4 hi = __builtin_bit_cast(f16x4, s.hi), lo = __builtin_bit_cast(f16x4, s.lo);
 #pragma unroll
-    for (int j = 0; j < Tile<W, PAIR>::kOutJ; ++j)
+    for (int i = 0; i < 4; ++i) x[i] = (float)hi[i] + (float)lo[i];
+}
+
+// A wavefront's sums row by row (of 16): get(j, b) loads what use(j, b) needs
+// of row j into b, a row ahead.  The compiler keeps a kernel's loads and stores
+// in order, so loaded one by one they would take a memory latency each.
+template <int W, bool PAIR, class Buffer, class Get, class Use>
+__device__ __forceinline__ void rows_ahead(Get &&get, Use &&use) {
+    constexpr int J = Tile<W, PAIR>::kOutJ;
+    Buffer b[2];
+    get(0, b[0]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t r = (int64_t)ti * Tile<W>::kSide + row0<W, PAIR>() + 16 * j;
-            const int64_t c = (int64_t)tj * Tile<W>::kSide + col0<W>() + 16 * i;
-            float x[4];
-            value(i, j, r, c, x);
-            uint2 hi, lo;
-            split4(x, hi, lo);
-            put_split4(base, split_at(r, c, ld), hi, lo);
-            if (ti != tj)
-                put_split4(base, split_at(c + (threadIdx.x & 3), r & ~(int64_t)3, ld), transpose4(hi), transpose4(lo));
-        }
+    for (int j = 0; j < J; ++j) {
+        if (j + 1 < J) get(j + 1, b[(j + 1) & 1]);
+        use(j, b[j & 1]);
+    }
+}
+
+// Stores row j of this wavefront's values x as part of tile (ti, tj) of the
+// symmetric n x n array at `base`, and transposed as part of tile (tj, ti).
+template <int W, bool PAIR>
+__device__ __forceinline__ void store_symmetric(char *base, int n, int ti, int tj, int i, int j, const float (&x)[4]) {
+    const int r = ti * Tile<W>::kSide + row0<W, PAIR>() + 16 * j, c = tj * Tile<W>::kSide + col0<W>() + 16 * i;
+    uint2 hi, lo;
+    split4(x, hi, lo);
+    const uint2 th = transpose4(hi), tl = transpose4(lo);
+    if (r >= n || c >= n) return;  // (the same in the four lanes of a block: n is a multiple of 32)
+    put_split4(base, split_at(r, c, n), hi, lo);
+    if (ti != tj) put_split4(base, split_at(c + (threadIdx.x & 3), r & ~3, n), th, tl);
 }
 
 // A = X X^T or X^T X
@@ -195,20 +212,26 @@ __global__ __launch_bounds__((Tile<W, PAIR>::kLanes), (Tile<W, PAIR>::kWavesPerS
     const MuonTile t = ma.sym[blockIdx.x];
     if (t.mat < 0) return;
     const MuonMat M = ma.mats[t.mat];
-    const char *X = ma.ws + M.x[from];
+    const char *X = ma.ws + (from ? M.x[1] : M.x[0]);
     const int64_t rows32 = split_rows32(M.ld);
     Sums<W> s{};
     if (M.tall)
-        product<W, PAIR, KR, KR, true, false>(column_feed<W>(X, t.i, rows32), rows32, column_feed<W>(X, t.j, rows32), rows32,
-                                           (M.rows + 31) / 32, lds_at(lds), s);
+        product<W, PAIR, KR, KR, true, false>(column_feed<W>(X, t.i, rows32, M.ld), rows32,
+                                              column_feed<W>(X, t.j, rows32, M.ld), rows32, (M.rows + 31) / 32, lds_at(lds),
+                                              s);
     else
-        product<W, PAIR, KC, KC, true, false>(row_feed<W>(X, t.i, rows32), kSplitBlock, row_feed<W>(X, t.j, rows32),
-                                           kSplitBlock, (M.cols + 31) / 32, lds_at(lds), s);
+        product<W, PAIR, KC, KC, true, false>(row_feed<W>(X, t.i, rows32, M.rp), kSplitBlock,
+                                              row_feed<W>(X, t.j, rows32, M.rp), kSplitBlock, (M.cols + 31) / 32, lds_at(lds), s);
     join_pair<W, PAIR>(lds_at(lds), s);
-    store_symmetric<W, PAIR>(ma.ws + M.a, M.sp, t.i, t.j, [&](int i, int j, int64_t, int64_t, float(&x)[4]) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = s.v[i][j][e] * kMuonUnscale;
-    });
+    for (int j = 0; j < Tile<W, PAIR>::kOutJ; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = s.v[i][j][e] * kMuonUnscale;
+            store_symmetric<W, PAIR>(ma.ws + M.a, M.sp, t.i, t.j, i, j, x);
+        }
 }
 
 // B = b A + c A A
@@ -222,14 +245,30 @@ __global__ __launch_bounds__((Tile<W, PAIR>::kLanes), (Tile<W, PAIR>::kWavesPerS
     const char *A = ma.ws + M.a;
     const int64_t rows32 = split_rows32(M.sp);
     Sums<W> s{};
-    product<W, PAIR, KC, KC, true, false>(row_feed<W>(A, t.i, rows32), kSplitBlock, row_feed<W>(A, t.j, rows32), kSplitBlock,
+    product<W, PAIR, KC, KC, true, false>(row_feed<W>(A, t.i, rows32, M.sp), kSplitBlock,
+                                          row_feed<W>(A, t.j, rows32, M.sp), kSplitBlock,
                                        ((M.tall ? M.cols : M.rows) + 31) / 32, lds_at(lds), s);
     join_pair<W, PAIR>(lds_at(lds), s);
-    store_symmetric<W, PAIR>(ma.ws + M.b, M.sp, t.i, t.j, [&](int i, int j, int64_t r, int64_t c, float(&x)[4]) {
-        load_split4(A, split_at(r, c, M.sp), x);
+    struct Row {
+        Split4 v[4];
+    };
+    const int r0 = t.i * Tile<W>::kSide + row0<W, PAIR>(), c0 = t.j * Tile<W>::kSide + col0<W>();
+    rows_ahead<W, PAIR, Row>(
+        [&](int j, Row &b) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = ma.qb * x[e] + ma.qc * (s.v[i][j][e] * kMuonUnscale);
-    });
+            for (int i = 0; i < 4; ++i)
+                if (r0 + 16 * j < M.sp && c0 + 16 * i < M.sp) b.v[i] = get_split4(A, split_at(r0 + 16 * j, c0 + 16 * i, M.sp));
+        },
+        [&](int j, const Row &b) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float x[4];
+                values(b.v[i], x);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = ma.qb * x[e] + ma.qc * (s.v[i][j][e] * kMuonUnscale);
+                store_symmetric<W, PAIR>(ma.ws + M.b, M.sp, t.i, t.j, i, j, x);
+            }
+        });
 }
 
 // X <- a X + B X or a X + X B
@@ -239,10 +278,12 @@ __device__ __forceinline__ void apply_product(const MuonArgs &ma, const MuonTile
     const int64_t x32 = split_rows32(M.ld), b32 = split_rows32(M.sp);
     const char *B = ma.ws + M.b;
     if (M.tall)
-        product<W, PAIR, KC, KC, true, false>(row_feed<W>(X, t.i, x32), kSplitBlock, row_feed<W>(B, t.j, b32), kSplitBlock,
+        product<W, PAIR, KC, KC, true, false>(row_feed<W>(X, t.i, x32, M.rp), kSplitBlock,
+                                              row_feed<W>(B, t.j, b32, M.sp), kSplitBlock,
                                            (M.cols + 31) / 32, lds, s);
     else
-        product<W, PAIR, KC, KR, true, false>(row_feed<W>(B, t.i, b32), kSplitBlock, column_feed<W>(X, t.j, x32), x32,
+        product<W, PAIR, KC, KR, true, false>(row_feed<W>(B, t.i, b32, M.sp), kSplitBlock,
+                                              column_feed<W>(X, t.j, x32, M.ld), x32,
                                            (M.rows + 31) / 32, lds, s);
     join_pair<W, PAIR>(lds, s);
 }
@@ -254,21 +295,30 @@ __global__ __launch_bounds__((Tile<W, PAIR>::kLanes), (Tile<W, PAIR>::kWavesPerS
     const MuonTile t = ma.full[blockIdx.x];
     if (t.mat < 0) return;
     const MuonMat M = ma.mats[t.mat];
-    const char *X = ma.ws + M.x[from];
-    char *Y = ma.ws + M.x[from ^ 1];
+    const char *X = ma.ws + (from ? M.x[1] : M.x[0]);
+    char *Y = ma.ws + (from ? M.x[0] : M.x[1]);
     Sums<W> s{};
     apply_product<W, PAIR>(ma, t, M, X, lds_at(lds), s);
+    struct Row {
+        Split4 v[4];
+    };
+    const int r0 = t.i * Tile<W>::kSide + row0<W, PAIR>(), c0 = t.j * Tile<W>::kSide + col0<W>();
+    rows_ahead<W, PAIR, Row>(
+        [&](int j, Row &b) {
 #pragma unroll
-    for (int j = 0; j < Tile<W, PAIR>::kOutJ; ++j)
+            for (int i = 0; i < 4; ++i)
+                if (r0 + 16 * j < M.rp && c0 + 16 * i < M.ld) b.v[i] = get_split4(X, split_at(r0 + 16 * j, c0 + 16 * i, M.ld));
+        },
+        [&](int j, const Row &b) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t at = split_at((int64_t)t.i * Tile<W>::kSide + row0<W, PAIR>() + 16 * j, (int64_t)t.j * Tile<W>::kSide + col0<W>() + 16 * i, M.ld);
-            float x[4];
-            load_split4(X, at, x);
+            for (int i = 0; i < 4; ++i) {
+                float x[4];
+                values(b.v[i], x);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = ma.qa * x[e] + s.v[i][j][e] * kMuonUnscale;
-            store_split4(Y, at, x);
-        }
+                for (int e = 0; e < 4; ++e) x[e] = ma.qa * x[e] + s.v[i][j][e] * kMuonUnscale;
+                if (r0 + 16 * j < M.rp && c0 + 16 * i < M.ld) store_split4(Y, split_at(r0 + 16 * j, c0 + 16 * i, M.ld), x);
+            }
+        });
 }
 
 template <int W, bool PAIR, int PK>
@@ -281,29 +331,62 @@ __global__ __launch_bounds__((Tile<W, PAIR>::kLanes), (Tile<W, PAIR>::kWavesPerS
     const MuonTile t = ma.full[blockIdx.x];
     if (t.mat < 0) return;
     const MuonMat M = ma.mats[t.mat];
-    const char *X = ma.ws + M.x[from];
+    const char *X = ma.ws + (from ? M.x[1] : M.x[0]);
     Sums<W> s{};
     apply_product<W, PAIR>(ma, t, M, X, lds_at(lds), s);
     const TensorDesc T = uniform_desc(a.tensors[M.tensor]);
     const double scale = muon_scale(ma.scale_kind, M.rows, M.cols);
     const float f = (float)(sc.lr64 * scale), lw = sc.lrwd[T.group];
     const bool vec = T.vec_ok && (M.cols & 3) == 0 && (M.elem0 & 3) == 0;
+    struct Row {
+        Split4 v[4];
+        float p[4][4];
+    };
+    const int r0 = t.i * Tile<W>::kSide + row0<W, PAIR>(), c0 = t.j * Tile<W>::kSide + col0<W>();
+    auto at = [&](int i, int j) { return M.elem0 + (int64_t)(r0 + 16 * j) * M.cols + c0 + 16 * i; };
+    auto left = [&](int i, int j) { return r0 + 16 * j < M.rows ? M.cols - c0 - 16 * i : 0; };  // elements of the row
+    rows_ahead<W, PAIR, Row>(
+        [&](int j, Row &b) {
 #pragma unroll
-    for (int j = 0; j < Tile<W, PAIR>::kOutJ; ++j)
+            for (int i = 0; i < 4; ++i) {
+                if (left(i, j) <= 0) continue;
+                b.v[i] = get_split4(X, split_at(r0 + 16 * j, c0 + 16 * i, M.ld));
+                if (vec && left(i, j) >= 4) {
+                    load_p<PK, 4, kStridedKeep>(T, at(i, j), b.p[i]);
+                } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int32_t rr = t.i * Tile<W>::kSide + row0<W, PAIR>() + 16 * j, cc = t.j * Tile<W>::kSide + col0<W>() + 16 * i;
-            if (rr >= M.rows || cc >= M.cols) continue;
-            float x[4];
-            load_split4(X, split_at(rr, cc, M.ld), x);
+                    for (int k = 0; k < 4; ++k)
+                        if (k < left(i, j)) {
+                            float p[1];
+                            load_p<PK, 1>(T, at(i, j) + k, p);
+                            b.p[i][k] = p[0];
+                        }
+                }
+            }
+        },
+        [&](int j, const Row &b) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = (ma.qa * x[e] + s.v[i][j][e] * kMuonUnscale) * kMuonUnscale;
-            const int64_t e = M.elem0 + (int64_t)rr * M.cols + cc;
-            if (vec && cc + 4 <= M.cols)
-                muon_update<PK, 4>(T, e, x, lw, f);
-            else
-                for (int k = 0; k < 4 && cc + k < M.cols; ++k) muon_update<PK, 1>(T, e + k, x + k, lw, f);
-        }
+            for (int i = 0; i < 4; ++i) {
+                if (left(i, j) <= 0) continue;
+                float x[4], p[4];
+                values(b.v[i], x);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[e] = (ma.qa * x[e] + s.v[i][j][e] * kMuonUnscale) * kMuonUnscale;
+                    p[e] = decayed(b.p[i][e], lw, f * x[e]);
+                }
+                if (vec && left(i, j) >= 4) {
+                    store_p<PK, 4, kStridedKeep>(T, at(i, j), p);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (k < left(i, j)) {
+                            const float y[1] = {p[k]};
+                            store_p<PK, 1>(T, at(i, j) + k, y);
+                        }
+                }
+            }
+        });
 }
 
 }  // namespace

@@ -32,7 +32,6 @@ struct Slab {
     static constexpr int kRowFrags = SP / 64;         // 16-row fragments of A of a wavefront
     static constexpr int kColFrags = SP / 16;
     static constexpr int kLongFrags = kLong / 64;     // 16-position fragments of X of a wavefront
-    static constexpr int kPerLane = kMuonSlab / kThreads;
 };
 
 // Byte of the 16-byte chunk holding value c (of 8) of row r, in an LDS array
@@ -146,9 +145,9 @@ __device__ __forceinline__ void slab_polynomial(const MuonArgs &ma, uint32_t as,
     __syncthreads();
 }
 
-// X <- a X + X B: a wavefront's own rows.  put(row, column, four values) takes them.
-template <int SP, class F>
-__device__ __forceinline__ void slab_apply(const MuonArgs &ma, uint32_t xs, uint32_t as, int side, int len, F &&put) {
+// X <- a X + X B in place: a wavefront's rows depend on its own rows alone.
+template <int SP>
+__device__ __forceinline__ void slab_apply(const MuonArgs &ma, uint32_t xs, uint32_t as, int side, int len) {
     using T = Slab<SP>;
 #pragma unroll
     for (int x = 0; x < T::kLongFrags; ++x) {
@@ -172,18 +171,21 @@ __device__ __forceinline__ void slab_apply(const MuonArgs &ma, uint32_t xs, uint
             slab_get4(xs, T::kLong, row, square_col(i), y);
 #pragma unroll
             for (int e = 0; e < 4; ++e) y[e] = ma.qa * y[e] + acc[i][e] * kMuonUnscale;
-            put(row, square_col(i), y);
+            slab_put4(xs, T::kLong, row, square_col(i), y);
         }
     }
 }
 
-// A matrix's shape as its slabs see it.
+// A matrix's shape as its slabs see it.  In memory the slab is `outer` runs of
+// `inner` elements, `cols` apart: a position's values (tall) or a value's
+// positions (wide).
 struct Shape {
     int64_t e0;     // element of the slab's first position, first value
     int32_t cols;   // elements between the matrix's rows
     int32_t side;   // the short side
     int32_t len;    // positions of this slab
     int32_t tall;
+    int32_t inner, outer;
 };
 template <int SP>
 __device__ __forceinline__ Shape slab_shape(const MuonMat &M, int32_t slab) {
@@ -194,18 +196,46 @@ __device__ __forceinline__ Shape slab_shape(const MuonMat &M, int32_t slab) {
     const int32_t left = (M.tall ? M.rows : M.cols) - slab * Slab<SP>::kLong;
     h.len = left < Slab<SP>::kLong ? left : Slab<SP>::kLong;
     h.e0 = M.elem0 + (int64_t)slab * Slab<SP>::kLong * (M.tall ? M.cols : 1);
+    h.inner = M.tall ? h.side : h.len;
+    h.outer = M.tall ? h.len : h.side;
     return h;
 }
-// Position and value of the slab's element k in memory order, and its place.
-__device__ __forceinline__ int64_t slab_element(const Shape &h, int32_t k, int32_t &row, int32_t &c) {
-    if (h.tall) {
-        row = k / h.side;
-        c = k - row * h.side;
-        return h.e0 + k;
+// A lane's way through the slab in memory order, V neighbouring elements at a
+// time, every kThreads-th such group: one division at the start (two an element
+// took more time than the memory).
+template <int V>
+struct Walk {
+    int32_t o, i;        // run, place in it
+    int32_t step_o, step_i, inner, outer, tall, cols;
+    int64_t e;
+    __device__ __forceinline__ explicit Walk(const Shape &h)
+        : inner(h.inner), outer(h.outer), tall(h.tall), cols(h.cols) {
+        const int32_t k = (int32_t)threadIdx.x * V;
+        o = k / inner;
+        i = k - o * inner;
+        step_o = kThreads * V / inner;
+        step_i = kThreads * V - step_o * inner;
+        e = h.e0 + (int64_t)o * cols + i;
     }
-    c = k / h.len;
-    row = k - c * h.len;
-    return h.e0 + (int64_t)c * h.cols + row;
+    __device__ __forceinline__ bool there() const { return o < outer; }
+    __device__ __forceinline__ void next() {
+        o += step_o;
+        i += step_i;
+        e += (int64_t)step_o * cols + step_i;
+        if (i >= inner) {
+            i -= inner;
+            ++o;
+            e += cols - inner;
+        }
+    }
+    __device__ __forceinline__ int32_t row(int k) const { return tall ? o : i + k; }  // position of element k of V
+    __device__ __forceinline__ int32_t value(int k) const { return tall ? i + k : o; }
+};
+// Groups of elements that a lane has under way: a batch is a memory latency.
+constexpr int kSlabBatch = 8;
+// Whether the slab's runs are whole aligned groups of 4.
+__device__ __forceinline__ bool slab_vec(const TensorDesc &D, const Shape &h) {
+    return D.vec_ok && ((h.inner | h.cols) & 3) == 0 && (h.e0 & 3) == 0;
 }
 
 __device__ __forceinline__ void slab_zero(uint32_t xs) {
@@ -219,46 +249,102 @@ __device__ __forceinline__ void slab_put1(uint32_t xs, int32_t row, int32_t c, f
     *lds_ptr<_Float16>(xs + slab_chunk(Slab<SP>::kLong, row, c, 1) + (c & 7) * 2) = lo;
 }
 
-// The update of four neighbouring values of a position.
-template <int PK>
-__device__ __forceinline__ void slab_update(const TensorDesc &T, const Shape &h, int row, int c, const float (&y)[4],
-                                            float lw, float f, bool vec) {
-    if (row >= h.len || c >= h.side) return;
-    float x[4];
+// Calls body(walk, gradients, momenta) for a lane's groups of V.
+template <int GK, int V, class F>
+__device__ __forceinline__ void slab_walk(const TensorDesc &D, const Shape &h, float s, F &&body) {
+    Walk<V> w(h);
+    while (w.there()) {
+        float g[kSlabBatch][V], m[kSlabBatch][V];
+        Walk<V> ahead = w;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = y[i] * kMuonUnscale;
-    if (h.tall) {
-        const int64_t e = h.e0 + (int64_t)row * h.cols + c;
-        if (vec && c + 4 <= h.side) {
-            muon_update<PK, 4>(T, e, x, lw, f);
-            return;
+        for (int k = 0; k < kSlabBatch; ++k) {
+            if (ahead.there()) {
+                load_g<GK, V>(D.g, ahead.e, s, g[k]);
+                ldf<V>(D.m, ahead.e, m[k]);
+            }
+            ahead.next();
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (c + i < h.side) muon_update<PK, 1>(T, e + i, x + i, lw, f);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (c + i < h.side) muon_update<PK, 1>(T, h.e0 + (int64_t)(c + i) * h.cols + row, x + i, lw, f);
+        for (int k = 0; k < kSlabBatch; ++k) {
+            if (w.there()) body(w, g[k], m[k]);
+            w.next();
+        }
     }
 }
-template <int PK>
-struct Update {
-    TensorDesc T;
-    Shape h;
-    float lw, f;
-    bool vec;
-    __device__ __forceinline__ Update(const StepArgs &a, const MuonArgs &ma, const MuonMat &M, const Shape &shape,
-                                      const Scalars &sc)
-        : T(uniform_desc(a.tensors[M.tensor])), h(shape) {
-        f = (float)(sc.lr64 * muon_scale(ma.scale_kind, M.rows, M.cols));
-        lw = sc.lrwd[T.group];
-        vec = T.vec_ok && (M.cols & 3) == 0 && (M.elem0 & 3) == 0;
+
+// m <- mu m + g; this lane's sum of u^2.
+template <int GK, int V>
+__device__ __forceinline__ double slab_momentum(const TensorDesc &D, const Shape &h, float s, float mu, int32_t nesterov) {
+    double acc = 0.0;
+    slab_walk<GK, V>(D, h, s, [&](const Walk<V> &w, const float(&g)[V], float(&m)[V]) {
+        float x[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) m[i] = mu * m[i] + g[i];
+        muon_u<V>(g, m, mu, nesterov, x);
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc = __builtin_fma((double)x[i], (double)x[i], acc);
+        stf<V>(D.m, w.e, m);
+    });
+    return acc;
+}
+// X0 from the new momentum, into zeroed LDS.
+template <int SP, int GK, int V>
+__device__ __forceinline__ void slab_fill(uint32_t xs, const TensorDesc &D, const Shape &h, float s, float mu,
+                                          int32_t nesterov, double f) {
+    slab_walk<GK, V>(D, h, s, [&](const Walk<V> &w, const float(&g)[V], float(&m)[V]) {
+        float x[V];
+        muon_u<V>(g, m, mu, nesterov, x);
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = (float)((double)x[i] * f);
+        if constexpr (V == 4) {
+            if (w.tall) {
+                slab_put4(xs, Slab<SP>::kLong, w.o, w.i, x);
+                return;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) slab_put1<SP>(xs, w.row(i), w.value(i), x[i]);
+    });
+}
+
+// The update, from the last X in LDS, in memory order and a batch at a time
+// (straight from the sums, a position's values would lie a row apart in a wide
+// matrix, and each load would wait for the store before it).
+template <int SP, int PK, int V>
+__device__ __forceinline__ void slab_update(const TensorDesc &D, const Shape &h, uint32_t xs, float lw, float f) {
+    Walk<V> w(h);
+    while (w.there()) {
+        float p[kSlabBatch][V];
+        Walk<V> ahead = w;
+#pragma unroll
+        for (int k = 0; k < kSlabBatch; ++k) {
+            if (ahead.there()) load_p<PK, V>(D, ahead.e, p[k]);
+            ahead.next();
+        }
+#pragma unroll
+        for (int k = 0; k < kSlabBatch; ++k) {
+            if (w.there()) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const int32_t r = w.row(i), c = w.value(i);
+                    const float hi = (float)*lds_ptr<const _Float16>(xs + slab_chunk(Slab<SP>::kLong, r, c, 0) + (c & 7) * 2);
+                    const float lo = (float)*lds_ptr<const _Float16>(xs + slab_chunk(Slab<SP>::kLong, r, c, 1) + (c & 7) * 2);
+                    p[k][i] = decayed(p[k][i], lw, f * ((hi + lo) * kMuonUnscale));
+                }
+                store_p<PK, V>(D, w.e, p[k]);
+            }
+            w.next();
+        }
     }
-    __device__ __forceinline__ void operator()(int row, int c, const float (&y)[4]) const {
-        slab_update<PK>(T, h, row, c, y, lw, f, vec);
-    }
-};
+}
+template <int SP, int PK>
+__device__ __forceinline__ void slab_update(const StepArgs &a, const MuonArgs &ma, const MuonMat &M, const Shape &h,
+                                            const Scalars &sc, uint32_t xs) {
+    const TensorDesc D = uniform_desc(a.tensors[M.tensor]);
+    const float f = (float)(sc.lr64 * muon_scale(ma.scale_kind, M.rows, M.cols)), lw = sc.lrwd[D.group];
+    if (slab_vec(D, h)) slab_update<SP, PK, 4>(D, h, xs, lw, f);
+    else slab_update<SP, PK, 1>(D, h, xs, lw, f);
+}
 
 // ---------------------------------------------------------------- one slab
 // The whole step of one matrix.
@@ -276,64 +362,25 @@ __global__ __launch_bounds__(kThreads) void muon_lone_kernel(StepArgs a, MuonArg
     if (sc.skip) return;
     const TensorDesc D = uniform_desc(a.tensors[M.tensor]);
     const float mu = uniform(sc.b1), s = uniform(sc.inv_scale);
-    const int32_t n = h.len * h.side;
-    float u[T::kPerLane];
-    double acc = 0.0;
-#pragma unroll
-    for (int k0 = 0; k0 < T::kPerLane; k0 += 8) {
-        float g[8][1], m[8][1];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int32_t at = (k0 + k) * kThreads + threadIdx.x;
-            int32_t row, c;
-            g[k][0] = m[k][0] = 0.0f;
-            if (at < n) {
-                const int64_t e = slab_element(h, at, row, c);
-                load_g<GK, 1>(D.g, e, s, g[k]);
-                ldf<1>(D.m, e, m[k]);
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int32_t at = (k0 + k) * kThreads + threadIdx.x;
-            float x[1];
-            m[k][0] = mu * m[k][0] + g[k][0];
-            muon_u<1>(g[k], m[k], mu, nesterov, x);
-            u[k0 + k] = x[0];
-            acc = __builtin_fma((double)x[0], (double)x[0], acc);
-            if (at < n) {
-                int32_t row, c;
-                stf<1>(D.m, slab_element(h, at, row, c), m[k]);
-            }
-        }
-    }
     slab_zero(xs);
+    const bool vec = slab_vec(D, h);
+    double acc = vec ? slab_momentum<GK, 4>(D, h, s, mu, nesterov) : slab_momentum<GK, 1>(D, h, s, mu, nesterov);
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) acc += __shfl_xor(acc, o);
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = acc;
     __syncthreads();
     const double f = muon_factor((red[0] + red[1]) + (red[2] + red[3]), a.prep.eps);
-#pragma unroll
-    for (int k = 0; k < T::kPerLane; ++k) {
-        const int32_t at = k * kThreads + threadIdx.x;
-        int32_t row, c;
-        if (at < n) {
-            slab_element(h, at, row, c);
-            slab_put1<SP>(xs, row, c, (float)((double)u[k] * f));
-        }
-    }
-    const Update<PK> update(a, ma, M, h, sc);
+    if (vec) slab_fill<SP, GK, 4>(xs, D, h, s, mu, nesterov, f);
+    else slab_fill<SP, GK, 1>(xs, D, h, s, mu, nesterov, f);
     for (int32_t i = 0; i < steps; ++i) {
         __syncthreads();
         Square<SP> A;
         slab_gram<SP>(xs, h.len, A);
         slab_polynomial<SP>(ma, as, A, h.side);
-        if (i + 1 < steps)
-            slab_apply<SP>(ma, xs, as, h.side, h.len,
-                           [&](int row, int c, const float(&y)[4]) { slab_put4(xs, T::kLong, row, c, y); });
-        else
-            slab_apply<SP>(ma, xs, as, h.side, h.len, update);
+        slab_apply<SP>(ma, xs, as, h.side, h.len);
     }
+    __syncthreads();
+    slab_update<SP, PK>(a, ma, M, h, sc, xs);
 }
 
 // ---------------------------------------------------------------- several slabs
@@ -372,39 +419,20 @@ __global__ __launch_bounds__(kThreads) void muon_slab_first_kernel(StepArgs a, M
     const TensorDesc D = uniform_desc(a.tensors[M.tensor]);
     const float mu = (float)a.prep.beta1, s = a.prep.inv_scale ? *a.prep.inv_scale : 1.0f;
     const double f = reinterpret_cast<const double *>(a.blockfac)[t.mat];
-    const int32_t n = h.len * h.side;
     slab_zero(xs);
     __syncthreads();
-    for (int32_t k0 = 0; k0 < n; k0 += 8 * kThreads) {
-        float g[8][1], m[8][1];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int32_t at = k0 + k * kThreads + threadIdx.x;
-            int32_t row, c;
-            if (at < n) {
-                const int64_t e = slab_element(h, at, row, c);
-                load_g<GK, 1>(D.g, e, s, g[k]);
-                ldf<1>(D.m, e, m[k]);
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int32_t at = k0 + k * kThreads + threadIdx.x;
-            int32_t row, c;
-            if (at < n) {
-                float x[1];
-                muon_u<1>(g[k], m[k], mu, nesterov, x);
-                slab_element(h, at, row, c);
-                slab_put1<SP>(xs, row, c, (float)((double)x[0] * f));
-            }
-        }
-    }
+    if (slab_vec(D, h)) slab_fill<SP, GK, 4>(xs, D, h, s, mu, nesterov, f);
+    else slab_fill<SP, GK, 1>(xs, D, h, s, mu, nesterov, f);
     __syncthreads();
     slab_save(slab_image(ma, M, t.i), xs);
     Square<SP> A;
     slab_gram<SP>(xs, h.len, A);
     slab_save_part<SP>(slab_part<SP>(ma, M, 0, t.i), A);
 }
+
+// Matrices of more than kSlabJoin slabs have their parts summed by a launch of
+// their own, into the first part; else every slab sums them itself.
+constexpr int32_t kSlabJoin = 4;
 
 // One iteration: X and the parts of A (set `set`) in, X and its part of the
 // next A (the other set) out, or the update (PK >= 0).
@@ -416,15 +444,16 @@ __global__ __launch_bounds__(kThreads) void muon_slab_kernel(StepArgs a, MuonArg
     const MuonTile t = ma.full[blockIdx.x];
     const MuonMat M = ma.mats[t.mat];
     const Shape h = slab_shape<SP>(M, t.i);
-    auto work = [&](auto &&update) {
+    auto work = [&](auto &&end) {
         char *image = slab_image(ma, M, t.i);
         u32x4 x[kMuonSlab / 4 / kThreads];
 #pragma unroll
         for (int k = 0; k < kMuonSlab / 4 / kThreads; ++k) x[k] = ((const GMEM u32x4 *)gp(image))[k * kThreads + threadIdx.x];
         Square<SP> A{};
         const float *part = slab_part<SP>(ma, M, set, 0);
+        const int32_t parts = M.slabs > kSlabJoin ? 1 : M.slabs;
 #pragma unroll 2
-        for (int32_t k = 0; k < M.slabs; ++k, part += SP * SP)
+        for (int32_t k = 0; k < parts; ++k, part += SP * SP)
 #pragma unroll
             for (int r = 0; r < T::kRowFrags; ++r)
 #pragma unroll
@@ -433,26 +462,47 @@ __global__ __launch_bounds__(kThreads) void muon_slab_kernel(StepArgs a, MuonArg
 #pragma unroll
         for (int k = 0; k < kMuonSlab / 4 / kThreads; ++k) *lds_ptr<u32x4>(xs + (k * kThreads + threadIdx.x) * 16) = x[k];
         slab_polynomial<SP>(ma, as, A, h.side);
-        if constexpr (PK >= 0) {
-            slab_apply<SP>(ma, xs, as, h.side, h.len, update);
-        } else {
-            slab_apply<SP>(ma, xs, as, h.side, h.len,
-                           [&](int row, int c, const float(&y)[4]) { slab_put4(xs, T::kLong, row, c, y); });
-            __syncthreads();
-            slab_save(image, xs);
-            slab_gram<SP>(xs, h.len, A);
-            slab_save_part<SP>(slab_part<SP>(ma, M, set ^ 1, t.i), A);
-        }
+        slab_apply<SP>(ma, xs, as, h.side, h.len);
+        __syncthreads();
+        end(image, A);
     };
     if constexpr (PK >= 0) {
         __shared__ Scalars sc;
         step_begin(a, sc);
         const StepCommit commit{a, sc};
         if (sc.skip) return;
-        work(Update<PK>(a, ma, M, h, sc));
+        work([&](char *, Square<SP> &) { slab_update<SP, PK>(a, ma, M, h, sc, xs); });
     } else {
         if (skipped(a)) return;
-        work(0);
+        work([&](char *image, Square<SP> &A) {
+            slab_save(image, xs);
+            slab_gram<SP>(xs, h.len, A);
+            slab_save_part<SP>(slab_part<SP>(ma, M, set ^ 1, t.i), A);
+        });
+    }
+}
+
+// The parts of A of the matrices of many slabs: 4 elements a lane, in the
+// parts' order, one workgroup for each slab of the table.
+template <int SP>
+__global__ __launch_bounds__(kThreads) void muon_slab_join_kernel(StepArgs a, MuonArgs ma, int32_t set) {
+    if (skipped(a)) return;
+    const MuonTile t = ma.full[blockIdx.x];
+    const MuonMat M = ma.mats[t.mat];
+    if (M.slabs <= kSlabJoin) return;
+    for (int32_t q = t.i * kThreads + threadIdx.x; q < SP * SP / 4; q += M.slabs * kThreads) {
+        float *part = slab_part<SP>(ma, M, set, 0) + q * 4;
+        f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+        int32_t k = 0;
+        for (; k + 8 <= M.slabs; k += 8) {
+            f32x4 y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = *(const GMEM f32x4 *)gp(part + (int64_t)(k + i) * SP * SP);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x = x + y[i];
+        }
+        for (; k < M.slabs; ++k) x = x + *(const GMEM f32x4 *)gp(part + (int64_t)k * SP * SP);
+        *(GMEM f32x4 *)gp(part) = x;
     }
 }
 
@@ -462,7 +512,7 @@ void launch_slab(const StepArgs &a, const MuonArgs &ma, int64_t n, int32_t set, 
 }
 
 template <int SP>
-void launch_slabs_of(const StepArgs &args, const MuonArgs &ma, int64_t n, int pk, int gk, int32_t steps,
+void launch_slabs_of(const StepArgs &args, const MuonArgs &ma, int64_t n, bool many, int pk, int gk, int32_t steps,
                      int32_t nesterov, bool commit, hipStream_t s) {
     if (n == 0) return;
     StepArgs a = args;
@@ -471,9 +521,16 @@ void launch_slabs_of(const StepArgs &args, const MuonArgs &ma, int64_t n, int pk
         LAUNCH_TRACED((muon_slab_first_kernel<SP, G_F32>), (unsigned)n, kThreads, s, a, ma, nesterov);
     else
         LAUNCH_TRACED((muon_slab_first_kernel<SP, G_BF16>), (unsigned)n, kThreads, s, a, ma, nesterov);
-    for (int32_t i = 0; i + 1 < steps; ++i) launch_slab<SP, -1>(a, ma, n, i & 1, s);
-    a.commit = commit;
+    auto join = [&](int32_t set) {
+        if (many) LAUNCH_TRACED(muon_slab_join_kernel<SP>, (unsigned)n, kThreads, s, a, ma, set);
+    };
+    for (int32_t i = 0; i + 1 < steps; ++i) {
+        join(i & 1);
+        launch_slab<SP, -1>(a, ma, n, i & 1, s);
+    }
     const int32_t set = (steps - 1) & 1;
+    join(set);
+    a.commit = commit;
     if (pk == P_F32) launch_slab<SP, P_F32>(a, ma, n, set, s);
     else if (pk == P_BF16R) launch_slab<SP, P_BF16R>(a, ma, n, set, s);
     else if (pk == P_MBF16) launch_slab<SP, P_MBF16>(a, ma, n, set, s);
@@ -511,9 +568,9 @@ hipError_t launch_muon_slabs(const StepArgs &a, const MuonArgs &args, const Muon
     MuonArgs ma = args;
     ma.full += R.full0;
     const int64_t rest = R.slabs - R.narrow;
-    launch_slabs_of<64>(a, ma, R.narrow, pk, gk, steps, nesterov, commit && rest == 0, s);
+    launch_slabs_of<64>(a, ma, R.narrow, R.most_slabs > kSlabJoin, pk, gk, steps, nesterov, commit && rest == 0, s);
     ma.full += R.narrow;
-    launch_slabs_of<128>(a, ma, rest, pk, gk, steps, nesterov, commit, s);
+    launch_slabs_of<128>(a, ma, rest, R.most_slabs > kSlabJoin, pk, gk, steps, nesterov, commit, s);
     return hipGetLastError();
 }
 

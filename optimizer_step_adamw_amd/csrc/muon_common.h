@@ -52,15 +52,5 @@ __device__ __forceinline__ double muon_factor(double sum, double eps) {
     return n == 0.0 ? 0.0 : (double)kMuonScale / n;
 }
 
-// p <- p - (lw p + f x) for N elements from e.
-template <int PK, int N>
-__device__ __forceinline__ void muon_update(const TensorDesc &T, int64_t e, const float *x, float lw, float f) {
-    float p[N];
-    load_p<PK, N>(T, e, p);
-#pragma unroll
-    for (int i = 0; i < N; ++i) p[i] = decayed(p[i], lw, f * x[i]);
-    store_p<PK, N>(T, e, p);
-}
-
 }  // namespace
 }  // namespace optim

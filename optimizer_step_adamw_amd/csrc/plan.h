@@ -205,7 +205,7 @@ static_assert(sizeof(GradItem) == 24, "GradItem layout");
 
 // Muon: a matrix of the list with its arrays in the workspace (byte offsets
 // from the region that the runs share).  X is held padded to rp x ld, A and B
-// to sp x sp, sides rounded up to whole product tiles.
+// to sp x sp, sides rounded up to multiples of 32.
 constexpr int kMuonTile = 128, kMuonWideTile = 256;
 constexpr int64_t kMuonUnit = 4096;  // elements of padded X per workgroup of the splitting pass
 // Matrices with a side of at most 128 go through slabs: kMuonSlab values of X
@@ -246,9 +246,9 @@ struct MuonRun {          // matrices [mat0, mat1) that share a run of launches
     // slabs of matrices of a short side of at most 64 (then 128): of `slabs`
     // in the table from full0 on, the first `narrow`; 0: products by tiles
     int64_t slabs, narrow;
-    int32_t wide;         // matrices padded to kMuonWideTile, else kMuonTile
+    int32_t wide;         // wide tiles
     int32_t pair_sym, pair_full;  // the others by two groups of wavefronts each
-    int32_t pad_;
+    int32_t most_slabs;   // of one matrix
 };
 
 // Workspace layout (byte offsets from the workspace base, 256-aligned).

@@ -101,12 +101,13 @@ __device__ __forceinline__ void feed_slot(int t, int &row, int &chunk) {
     chunk = at % kChunks ^ (O == KC ? row & 7 : kr_swizzle(row));
 }
 // src: the operand's first byte (KC: row 0 of the tile; KR: column 0 of the
-// tile in the first row).  Split: ld is split_rows32().  Plain (KR): ld is the
-// bytes between rows, and chunks the 16-byte chunks of a row that exist (the
-// last one stands in for those behind it, whose columns are not stored).
-// (Offsets within a step stay below 2^32.)
+// tile in the first row).  Split: ld is split_rows32(), and left the rows (KC)
+// or columns (KR) from there on that exist, a multiple of 32; plain (KR): ld is
+// the bytes between rows, left the columns, a multiple of 8.  The last one
+// stands in for those behind it, whose sums are not stored.  (Offsets within a
+// step stay below 2^32.)
 template <int W, Order O, bool SPLIT>
-__device__ __forceinline__ Feed feed(const char *src, int64_t ld, int chunks = 64) {
+__device__ __forceinline__ Feed feed(const char *src, int64_t ld, int left) {
     Feed f;
     f.base = uniform_ptr(src);
 #pragma unroll
@@ -114,11 +115,13 @@ __device__ __forceinline__ Feed feed(const char *src, int64_t ld, int chunks = 6
         int row, chunk;
         feed_slot<W, O, SPLIT>(t, row, chunk);
         if constexpr (SPLIT && O == KC) {
+            if (row >= left) row = left - 1;
             f.at[t] = (uint32_t)((row >> 5) * ld + (row & 31) * 128 + chunk * 16);
         } else if constexpr (SPLIT) {
+            if ((chunk >> 3) * 32 >= left) chunk = (left / 32 - 1) * 8 + (chunk & 7);
             f.at[t] = (uint32_t)((chunk >> 3) * kSplitBlock + row * 128 + (chunk & 7) * 16);
         } else {
-            if (chunk >= chunks) chunk = chunks - 1;
+            if (chunk * 8 >= left) chunk = left / 8 - 1;
             f.at[t] = (uint32_t)(row * ld + chunk * 16);
         }
     }
