@@ -127,10 +127,10 @@ struct Built {
     std::vector<int32_t> pack_off;
     std::vector<PackMember> pack_td;
     int64_t pack_unit0 = 0;         // first pack unit (packs come last)
-    std::vector<GradTensor> gtensors;  // gradient lists
-    std::vector<GradItem> gitems;
-    std::vector<int32_t> gorder;
+    std::vector<GradItem> gitems;      // gradient lists
+    std::vector<GradSmall> gsmall;
     int64_t gbytes = 0;
+    int32_t gkeep0 = 0;
     std::vector<MuonMat> mats;      // Muon
     std::vector<MuonTile> sym, full;
     std::vector<MuonRun> runs;
@@ -420,7 +420,6 @@ int build_grads(const optim_tensor_list *list, const optim_plan_opts *opts, Buil
     if (n > 0 && (!list->numel || !list->grad)) return fail(OPTIM_EINVAL, "numel and grad arrays are required");
     const size_t gsz = list->grad_dtype == OPTIM_F32 ? 4 : 2;
     std::vector<Range> ranges;
-    B.gtensors.assign(n, GradTensor{});
     for (int i = 0; i < n; ++i) {
         const std::string ti = "tensor " + std::to_string(i) + ": ";
         const int64_t numel = list->numel[i];
@@ -429,38 +428,41 @@ int build_grads(const optim_tensor_list *list, const optim_plan_opts *opts, Buil
         void *g = const_cast<void *>(list->grad[i]);
         if (numel > 0 && !g) return fail(OPTIM_EINVAL, ti + "NULL grad");
         if (!aligned(g, gsz)) return fail(OPTIM_EALIGN, ti + "grad misaligned");
-        GradTensor &T = B.gtensors[i];
-        T.g = g;
-        T.numel = numel;
         if (numel == 0) continue;
         ranges.push_back({(uintptr_t)g, (uintptr_t)g + (size_t)numel * gsz, true, i, "grad"});
         B.gbytes += numel * (int64_t)gsz;
+    }
+    int64_t item = kGradItemMax;
+    while (item > kGradItemMin && B.gbytes < item * kGradItems) item /= 2;
+    item /= (int64_t)gsz;  // elements
+    for (int i = 0; i < n; ++i) {
+        const int64_t numel = list->numel[i];
+        if (numel == 0) continue;
+        char *g = static_cast<char *>(const_cast<void *>(list->grad[i]));
         if (numel <= kGradSmall) {
-            B.gorder.push_back(i);
+            B.gsmall.push_back(GradSmall{g, i, (int32_t)numel});
             continue;
         }
-        const int64_t items = (numel + kGradItem - 1) / kGradItem;
-        if (items + (int64_t)B.gitems.size() >= INT32_MAX) return fail(OPTIM_EUNSUPPORTED, "gradient list too long");
-        T.slot0 = B.npartials;
-        T.nslots = (int32_t)items;
-        if (items > 1) B.npartials += items;
+        const int64_t items = (numel + item - 1) / item;
+        if (items + (int64_t)B.gitems.size() + n >= INT32_MAX) return fail(OPTIM_EUNSUPPORTED, "gradient list too long");
         for (int64_t k = 0; k < items; ++k)
-            B.gitems.push_back(GradItem{k * kGradItem, i, (int32_t)std::min(kGradItem, numel - k * kGradItem), (int32_t)k, 0});
+            B.gitems.push_back(GradItem{g + k * item * (int64_t)gsz, B.npartials, i,
+                                        (int32_t)std::min(item, numel - k * item), (int32_t)k, (int32_t)items});
+        if (items > 1) B.npartials += items;
     }
-    const int32_t small = (int32_t)B.gorder.size();
-    for (int32_t k = 0; k < small; k += kGradBundle)
-        B.gitems.push_back(GradItem{0, k, 0, 0, std::min(kGradBundle, small - k)});
+    int64_t kept = 0;
+    B.gkeep0 = (int32_t)B.gitems.size();
+    while (B.gkeep0 > 0 && kept < kGradKeepBytes) kept += B.gitems[--B.gkeep0].len * (int64_t)gsz;
     if (const int rc = check_overlaps(ranges)) return rc;
 
     Layout &L = B.L;
     size_t off = 0;
     L.counters = off; off += align256(kCounterBytes);
     L.group_wd = L.tensors = L.spans = L.codebook = L.blockspan = L.packs = L.pack_off = L.pack_td = L.blockfac = off;
-    L.gtensors = off; off += align256(std::max<size_t>(1, B.gtensors.size()) * sizeof(GradTensor));
     L.gitems = off; off += align256(std::max<size_t>(1, B.gitems.size()) * sizeof(GradItem));
-    L.gorder = off; off += align256(std::max<size_t>(1, B.gorder.size()) * sizeof(int32_t));
-    L.gcount = off; off += align256(std::max<size_t>(1, B.gtensors.size()) * sizeof(uint32_t));
-    L.gsum = off; off += align256(std::max<size_t>(1, B.gtensors.size()) * sizeof(double));
+    L.gsmall = off; off += align256(std::max<size_t>(1, B.gsmall.size()) * sizeof(GradSmall));
+    L.gcount = off; off += align256(std::max<size_t>(1, (size_t)n) * sizeof(uint32_t));
+    L.gsum = off; off += align256(std::max<size_t>(1, (size_t)n) * sizeof(double));
     L.partials = off;  // the uploaded image ends here
     off += align256(std::max<int64_t>(1, B.npartials) * sizeof(double));
     L.total = off;
@@ -896,8 +898,8 @@ struct optim_plan {
     uint64_t static_gen;
     Trace *trace;  // kernel trace (optim_plan_trace), or NULL
     int64_t pack_unit0;  // first pack unit
-    int32_t ngrads, ngitems;  // gradient lists: tensors, items
-    int64_t gbytes;           // bytes of all gradients
+    int32_t ngrads, ngitems, ngsmall;  // gradient lists: tensors, items, small tensors
+    int32_t gkeep0;           // first item that is left in the cache
 };
 
 extern "C" {
@@ -1012,9 +1014,8 @@ int create_on(const Built &B, const optim_tensor_list *list, int32_t algo, const
     std::memcpy(img.data() + B.L.mats, B.mats.data(), B.mats.size() * sizeof(MuonMat));
     std::memcpy(img.data() + B.L.sym, B.sym.data(), B.sym.size() * sizeof(MuonTile));
     std::memcpy(img.data() + B.L.full, B.full.data(), B.full.size() * sizeof(MuonTile));
-    std::memcpy(img.data() + B.L.gtensors, B.gtensors.data(), B.gtensors.size() * sizeof(GradTensor));
     std::memcpy(img.data() + B.L.gitems, B.gitems.data(), B.gitems.size() * sizeof(GradItem));
-    std::memcpy(img.data() + B.L.gorder, B.gorder.data(), B.gorder.size() * sizeof(int32_t));
+    std::memcpy(img.data() + B.L.gsmall, B.gsmall.data(), B.gsmall.size() * sizeof(GradSmall));
     if (is_blockwise(algo)) {
         Codebook *cb = reinterpret_cast<Codebook *>(img.data() + B.L.codebook);
         if (!build_map(7, cb->m8) || !build_map(8, cb->v8) || !build_map(3, cb->m4) || !build_map(4, cb->v4))
@@ -1056,9 +1057,10 @@ int create_on(const Built &B, const optim_tensor_list *list, int32_t algo, const
     P->static_dev = dev;
     P->static_gen = 0;
     P->pack_unit0 = B.pack_unit0;
-    P->ngrads = (int32_t)B.gtensors.size();
+    P->ngrads = list->n;
     P->ngitems = (int32_t)B.gitems.size();
-    P->gbytes = B.gbytes;
+    P->ngsmall = (int32_t)B.gsmall.size();
+    P->gkeep0 = B.gkeep0;
     *out = P;
     return OPTIM_OK;
 }
@@ -1312,16 +1314,16 @@ int check_expert_sizes(int32_t experts, int64_t tokens, int64_t m, int64_t n) {
 
 GradArgs grad_args(optim_plan *P) {
     GradArgs a{};
-    a.tensors = reinterpret_cast<const GradTensor *>(P->ws + P->L.gtensors);
     a.items = reinterpret_cast<const GradItem *>(P->ws + P->L.gitems);
-    a.order = reinterpret_cast<const int32_t *>(P->ws + P->L.gorder);
+    a.small = reinterpret_cast<const GradSmall *>(P->ws + P->L.gsmall);
     a.count = reinterpret_cast<uint32_t *>(P->ws + P->L.gcount);
     a.done = reinterpret_cast<uint32_t *>(P->ws + P->L.counters);
     a.partials = reinterpret_cast<double *>(P->ws + P->L.partials);
     a.sums = reinterpret_cast<double *>(P->ws + P->L.gsum);
     a.ntensors = P->ngrads;
     a.nitems = P->ngitems;
-    a.keep = P->gbytes <= kGradKeepBytes;
+    a.nsmall = P->ngsmall;
+    a.keep0 = P->gkeep0;
     return a;
 }
 

@@ -177,31 +177,37 @@ constexpr size_t kCounterBytes = (1 + kSubCounters) * kCounterStride * sizeof(ui
 constexpr int kAmaxSlots = 16;
 constexpr size_t kAmaxBytesPerBlock = 2 * kAmaxSlots * kCounterStride * sizeof(uint32_t);
 
-// Gradient lists (OPTIM_ALGO_GRADS): one workgroup per item.  An item is
-// either up to kGradItem elements of one tensor, or a bundle of whole small
-// tensors, which the workgroup's wavefronts take one each at a time.
-constexpr int64_t kGradItem = 32768;
-constexpr int64_t kGradSmall = 4096;   // tensors of at most this many elements are bundled
-constexpr int32_t kGradBundle = 16;    // tensors per bundle at most
-// lists of at most this many bytes are left in the 256 MB Infinity Cache by
-// the norms' read, for the clip that follows
+// Gradient lists (OPTIM_ALGO_GRADS): a workgroup takes an item, a run of one
+// tensor's elements, or four small tensors, one per wavefront (6000 vectors
+// took 19.8 us so, and 22.4 with 16 a workgroup, when both were measured).
+// Items are of kGradItemMax bytes, halved down to kGradItemMin while the list
+// has fewer than kGradItems of them.  Measured: 1.1B bf16 430 us with 64 KiB,
+// 397 with 128, 390 with 256; 4096 x 4096 fp32 with its clip 49 us with 64 KiB
+// (1024 items), 45 with 128, 43 with 256, 49 with 512.
+constexpr int64_t kGradItemMax = 256 << 10;
+constexpr int64_t kGradItemMin = 64 << 10;
+constexpr int64_t kGradItems = 256;
+constexpr int64_t kGradSmall = 4096;   // elements of a small tensor at most
+// The list's last bytes are read with ordinary loads, the others non-temporal:
+// they stay in the 256 MB Infinity Cache for the clip that follows.  Measured,
+// nothing kept, these last bytes, all: norms and clip of 67 MB 49, 43, 43 us,
+// of 1.3 GB 577, 569, 573; norms alone of 2.3 GB 380, 373, 412.
 constexpr int64_t kGradKeepBytes = int64_t(256) << 20;
-struct GradTensor {       // 32 bytes
-    void *g;
-    int64_t numel;
-    int64_t slot0;        // first partial sum (tensors of more than one item)
-    int32_t nslots;       // items of the tensor (0: bundled or empty)
-    int32_t pad_;
-};
-static_assert(sizeof(GradTensor) == 32, "GradTensor layout");
-struct GradItem {         // 24 bytes
-    int64_t start;        // first element (single tensor)
-    int32_t tensor;       // its tensor; bundle: its first place in `order`
-    int32_t len;          // elements; bundle: 0
+struct GradItem {         // 32 bytes
+    void *g;              // its first element
+    int64_t slot0;        // the tensor's first partial sum
+    int32_t tensor;
+    int32_t len;          // elements
     int32_t slot;         // which of the tensor's items this is
-    int32_t count;        // bundle: tensors
+    int32_t nslots;       // how many it has
 };
-static_assert(sizeof(GradItem) == 24, "GradItem layout");
+static_assert(sizeof(GradItem) == 32, "GradItem layout");
+struct GradSmall {        // 16 bytes
+    void *g;
+    int32_t tensor;
+    int32_t len;
+};
+static_assert(sizeof(GradSmall) == 16, "GradSmall layout");
 
 // Muon: a matrix of the list with its arrays in the workspace (byte offsets
 // from the region that the runs share).  X is held padded to rp x ld, A and B
@@ -258,7 +264,7 @@ struct Layout {
         blockspan, packs, pack_off, pack_td, total;
     // gradient lists: tensors, items, the bundled tensors' indexes, arrival
     // counters and sums of the tensors
-    size_t gtensors, gitems, gorder, gcount, gsum;
+    size_t gitems, gsmall, gcount, gsum;
     // Muon: matrices, tiles of the symmetric products and of X, the region
     // the runs share
     size_t mats, sym, full, muon;
@@ -405,16 +411,16 @@ hipError_t launch_muon(const StepArgs &a, const MuonArgs &ma, int pk, int gk, in
 
 // Gradient lists (kernels_grads.hip).  kind: OPTIM_NORM_*.
 struct GradArgs {
-    const GradTensor *tensors;
     const GradItem *items;
-    const int32_t *order;  // indexes of the bundled tensors
+    const GradSmall *small;
     uint32_t *count;       // per tensor: items that have arrived, 0 between calls
     uint32_t *done;        // arrival counters of the launch, 0 between calls
     double *partials;      // one per item of a tensor of several
     double *sums;          // one per tensor
     int32_t ntensors;
     int32_t nitems;
-    int32_t keep;          // the list is read again soon: leave it in the cache
+    int32_t nsmall;
+    int32_t keep0;         // items from here on are left in the cache
 };
 hipError_t launch_grad_norms(const GradArgs &a, int gk, int kind, const float *inv_scale, double max_norm,
                              float *found_inf, float *norms, float *total, float *coef, hipStream_t s);
