@@ -261,6 +261,41 @@ void add_product(const Built &B, const MuonRun &R, bool upper, std::vector<MuonT
     narrow = (int64_t)out.size() - first - wide;
 }
 
+// The pieces of the sums of A and A A (see kMuonPieceMin); partial sums as 128 x
+// 128 tiles of fp32 [piece][tile row][tile column].  (Decided for the plan too.)
+void add_pieces(Built &B) {
+    auto steps = [](const MuonMat &M, int k) { return (int64_t)((k ? M.sp : std::max(M.rp, M.ld)) / 32); };
+    int64_t total[2] = {0, 0}, longest[2] = {0, 0}, piece[2];
+    for (int k = 0; k < 2; ++k) {
+        for (const MuonMat &M : B.mats) {
+            if (M.slabs) continue;
+            const int64_t nt = count_of(M.sp, kMuonTile);
+            total[k] += nt * (nt + 1) / 2 * steps(M, k);
+            longest[k] = std::max(longest[k], steps(M, k));
+        }
+        piece[k] = std::max(kMuonPieceMin, count_of(total[k], kMuonSlots));
+    }
+    int64_t most = 0;
+    for (MuonRun &R : B.runs) {
+        R.most_parts[0] = R.most_parts[1] = 1;
+        int64_t used = 0;
+        for (int32_t m = R.mat0; m < R.mat1; ++m) {
+            MuonMat &M = B.mats[m];
+            M.part = B.muon_bytes + used;
+            for (int k = 0; k < 2; ++k) {
+                M.parts[k] = 1;
+                if (!R.slabs && !R.wide && longest[k] >= piece[k] + kMuonPieceGain)
+                    M.parts[k] = (int32_t)std::max<int64_t>(1, steps(M, k) / piece[k]);
+                R.most_parts[k] = std::max(R.most_parts[k], M.parts[k]);
+            }
+            const int64_t nt = count_of(M.sp, kMuonTile), parts = std::max(M.parts[0], M.parts[1]);
+            if (parts > 1) used += parts * nt * nt * kMuonTile * kMuonTile * 4;
+        }
+        most = std::max(most, used);
+    }
+    B.muon_bytes += most;
+}
+
 // The tile tables of the runs, from their matrices.  Plans whose products
 // have fewer narrow tiles than there are compute units give each tile two
 // groups of wavefronts.  (Decided for the plan, not run by run: the groups sum
@@ -285,6 +320,7 @@ void add_tiles(Built &B) {
         R.pair_sym = sym <= kMuonSlots;
         R.pair_full = full <= kMuonSlots;
     }
+    add_pieces(B);
 }
 
 // How a matrix is multiplied: by wide tiles, by tiles, through several slabs or

@@ -773,11 +773,12 @@ inline bool keep_for_second_pass(const StepArgs &a, int64_t reread_bytes_per_ele
 // trace the kernel's own start and end stamp the trace's next event pair.
 #define LAUNCH_TRACED(K, grid, block, s, ...)                                                      \
     do {                                                                                           \
-        TraceRec *tr_ = trace_slot(#K, (int64_t)(grid));                                           \
+        const dim3 g_(grid);                                                                       \
+        TraceRec *tr_ = trace_slot(#K, (int64_t)g_.x * g_.y);                                      \
         if (tr_)                                                                                   \
-            hipExtLaunchKernelGGL(K, dim3(grid), dim3(block), 0, s, tr_->start, tr_->stop, 0, __VA_ARGS__); \
+            hipExtLaunchKernelGGL(K, g_, dim3(block), 0, s, tr_->start, tr_->stop, 0, __VA_ARGS__);    \
         else                                                                                       \
-            hipLaunchKernelGGL(K, dim3(grid), dim3(block), 0, s, __VA_ARGS__);                    \
+            hipLaunchKernelGGL(K, g_, dim3(block), 0, s, __VA_ARGS__);                             \
     } while (0)
 
 #define LAUNCH_PERSISTENT(K, a, s) LAUNCH_TRACED(K, persistent_grid(K, a), kThreads, s, a)

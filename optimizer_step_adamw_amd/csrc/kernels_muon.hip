@@ -191,20 +191,42 @@ __device__ __forceinline__ void rows_ahead(Get &&get, Use &&use) {
     }
 }
 
-// Stores row j of this wavefront's values x as part of tile (ti, tj) of the
-// symmetric n x n array at `base`, and transposed as part of tile (tj, ti).
-template <int W, bool PAIR>
-__device__ __forceinline__ void store_symmetric(char *base, int n, int ti, int tj, int i, int j, const float (&x)[4]) {
-    const int r = ti * Tile<W>::kSide + row0<W, PAIR>() + 16 * j, c = tj * Tile<W>::kSide + col0<W>() + 16 * i;
+// Stores the values x of row r from column c on, of the symmetric n x n array
+// at `base`; four neighbouring lanes hold the rows of a 4 x 4 block.  Above the
+// diagonal blocks of 128 they are stored transposed too, below not at all: the
+// same in wide and narrow tiles, whose (r, c) and (c, r), off by a rounding,
+// would otherwise make a result depend on how the tiles were shared out.
+__device__ __forceinline__ void store_symmetric(char *base, int n, int r, int c, const float (&x)[4]) {
     uint2 hi, lo;
     split4(x, hi, lo);
     const uint2 th = transpose4(hi), tl = transpose4(lo);
-    if (r >= n || c >= n) return;  // (the same in the four lanes of a block: n is a multiple of 32)
+    // (the same in the four lanes of a block: n is a multiple of 32)
+    if (r >= n || c >= n || r / kMuonTile > c / kMuonTile) return;
     put_split4(base, split_at(r, c, n), hi, lo);
-    if (ti != tj) put_split4(base, split_at(c + (threadIdx.x & 3), r & ~3, n), th, tl);
+    if (r / kMuonTile != c / kMuonTile) put_split4(base, split_at(c + (threadIdx.x & 3), r & ~3, n), th, tl);
 }
 
-// A = X X^T or X^T X
+// Partial sums of piece `part` of tile (i, j) of A or A A, row-major.
+__device__ __forceinline__ float *piece_sums(const MuonArgs &ma, const MuonMat &M, const MuonTile &t, int part) {
+    const int nt = (M.sp + kMuonTile - 1) / kMuonTile;
+    return reinterpret_cast<float *>(ma.ws + M.part) + (((int64_t)part * nt + t.i) * nt + t.j) * kMuonTile * kMuonTile;
+}
+template <bool PAIR>
+__device__ __forceinline__ void store_piece(float *at, const Sums<1> &s) {
+    GMEM float *q = gp(at) + row0<1, PAIR>() * kMuonTile + col0<1>();
+#pragma unroll
+    for (int j = 0; j < Tile<1, PAIR>::kOutJ; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *(GMEM f32x4 *)(q + 16 * j * kMuonTile + 16 * i) = s.v[i][j];
+}
+// Steps of piece blockIdx.y of `parts` of a sum of `all`, and where it begins.
+__device__ __forceinline__ int piece_steps(int all, int parts, int &first) {
+    const int each = (all + parts - 1) / parts;
+    first = (int)blockIdx.y * each;
+    return all - first < each ? all - first : each;
+}
+
+// A = X X^T or X^T X, or the sums over a piece of the longer side
 template <int W, bool PAIR>
 __global__ __launch_bounds__((Tile<W, PAIR>::kLanes), (Tile<W, PAIR>::kWavesPerSimd)) void muon_gram_kernel(StepArgs a, MuonArgs ma, int32_t from) {
     __shared__ __align__(1024) char lds[Tile<W, PAIR>::kLds];
@@ -212,17 +234,23 @@ __global__ __launch_bounds__((Tile<W, PAIR>::kLanes), (Tile<W, PAIR>::kWavesPerS
     const MuonTile t = ma.sym[blockIdx.x];
     if (t.mat < 0) return;
     const MuonMat M = ma.mats[t.mat];
+    if ((int)blockIdx.y >= M.parts[0]) return;
     const char *X = ma.ws + (from ? M.x[1] : M.x[0]);
-    const int64_t rows32 = split_rows32(M.ld);
+    const int64_t rows32 = split_rows32(M.ld), step = M.tall ? rows32 : kSplitBlock;
+    int first;
+    const int steps = piece_steps(((M.tall ? M.rows : M.cols) + 31) / 32, M.parts[0], first);
+    X += first * step;
     Sums<W> s{};
     if (M.tall)
-        product<W, PAIR, KR, KR, true, false>(column_feed<W>(X, t.i, rows32, M.ld), rows32,
-                                              column_feed<W>(X, t.j, rows32, M.ld), rows32, (M.rows + 31) / 32, lds_at(lds),
-                                              s);
+        product<W, PAIR, KR, KR, true, false>(column_feed<W>(X, t.i, rows32, M.ld), step,
+                                              column_feed<W>(X, t.j, rows32, M.ld), step, steps, lds_at(lds), s);
     else
-        product<W, PAIR, KC, KC, true, false>(row_feed<W>(X, t.i, rows32, M.rp), kSplitBlock,
-                                              row_feed<W>(X, t.j, rows32, M.rp), kSplitBlock, (M.cols + 31) / 32, lds_at(lds), s);
+        product<W, PAIR, KC, KC, true, false>(row_feed<W>(X, t.i, rows32, M.rp), step, row_feed<W>(X, t.j, rows32, M.rp),
+                                              step, steps, lds_at(lds), s);
     join_pair<W, PAIR>(lds_at(lds), s);
+    const int r0 = row0<W, PAIR>(), c0 = col0<W>();
+    if constexpr (W == 1)
+        if (M.parts[0] > 1) return store_piece<PAIR>(piece_sums(ma, M, t, blockIdx.y), s);
 #pragma unroll
     for (int j = 0; j < Tile<W, PAIR>::kOutJ; ++j)
 #pragma unroll
@@ -230,11 +258,11 @@ __global__ __launch_bounds__((Tile<W, PAIR>::kLanes), (Tile<W, PAIR>::kWavesPerS
             float x[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[e] = s.v[i][j][e] * kMuonUnscale;
-            store_symmetric<W, PAIR>(ma.ws + M.a, M.sp, t.i, t.j, i, j, x);
+            store_symmetric(ma.ws + M.a, M.sp, t.i * Tile<W>::kSide + r0 + 16 * j, t.j * Tile<W>::kSide + c0 + 16 * i, x);
         }
 }
 
-// B = b A + c A A
+// B = b A + c A A, or the sums over a piece of A A
 template <int W, bool PAIR>
 __global__ __launch_bounds__((Tile<W, PAIR>::kLanes), (Tile<W, PAIR>::kWavesPerSimd)) void muon_square_kernel(StepArgs a, MuonArgs ma) {
     __shared__ __align__(1024) char lds[Tile<W, PAIR>::kLds];
@@ -242,13 +270,18 @@ __global__ __launch_bounds__((Tile<W, PAIR>::kLanes), (Tile<W, PAIR>::kWavesPerS
     const MuonTile t = ma.sym[blockIdx.x];
     if (t.mat < 0) return;
     const MuonMat M = ma.mats[t.mat];
+    if ((int)blockIdx.y >= M.parts[1]) return;
     const char *A = ma.ws + M.a;
     const int64_t rows32 = split_rows32(M.sp);
+    int first;
+    const int steps = piece_steps(((M.tall ? M.cols : M.rows) + 31) / 32, M.parts[1], first);
+    const char *P = A + first * kSplitBlock;
     Sums<W> s{};
-    product<W, PAIR, KC, KC, true, false>(row_feed<W>(A, t.i, rows32, M.sp), kSplitBlock,
-                                          row_feed<W>(A, t.j, rows32, M.sp), kSplitBlock,
-                                       ((M.tall ? M.cols : M.rows) + 31) / 32, lds_at(lds), s);
+    product<W, PAIR, KC, KC, true, false>(row_feed<W>(P, t.i, rows32, M.sp), kSplitBlock,
+                                          row_feed<W>(P, t.j, rows32, M.sp), kSplitBlock, steps, lds_at(lds), s);
     join_pair<W, PAIR>(lds_at(lds), s);
+    if constexpr (W == 1)
+        if (M.parts[1] > 1) return store_piece<PAIR>(piece_sums(ma, M, t, blockIdx.y), s);
     struct Row {
         Split4 v[4];
     };
@@ -266,9 +299,57 @@ __global__ __launch_bounds__((Tile<W, PAIR>::kLanes), (Tile<W, PAIR>::kWavesPerS
                 values(b.v[i], x);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[e] = ma.qb * x[e] + ma.qc * (s.v[i][j][e] * kMuonUnscale);
-                store_symmetric<W, PAIR>(ma.ws + M.b, M.sp, t.i, t.j, i, j, x);
+                store_symmetric(ma.ws + M.b, M.sp, r0 + 16 * j, c0 + 16 * i, x);
             }
         });
+}
+
+// Joins the pieces of tiles of A or A A, in their order: a quarter of a tile's
+// rows per workgroup.
+template <bool SQUARE>
+__global__ __launch_bounds__(kThreads) void muon_join_kernel(StepArgs a, MuonArgs ma) {
+    if (skipped(a)) return;
+    const MuonTile t = ma.sym[blockIdx.x];
+    if (t.mat < 0) return;
+    const MuonMat M = ma.mats[t.mat];
+    const int parts = M.parts[SQUARE];
+    if (parts <= 1) return;
+    const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int r = blockIdx.y * 32 + (w & 1) * 16 + (lane & 15), c = (w >> 1) * 64 + (lane >> 4) * 4;
+    const int64_t apart = piece_sums(ma, M, MuonTile{}, 1) - piece_sums(ma, M, MuonTile{}, 0);
+    const GMEM float *q = gp(piece_sums(ma, M, t, 0)) + r * kMuonTile + c;
+    f32x4 sum[4] = {};
+    constexpr int U = 4;  // pieces under way
+    for (int p = 0; p < parts; p += U) {
+        f32x4 v[U][4];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (p + u < parts) v[u][i] = *(const GMEM f32x4 *)(q + (p + u) * apart + 16 * i);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (p + u < parts) sum[i] += v[u][i];
+    }
+    const int rt = t.i * kMuonTile + r, ct = t.j * kMuonTile + c;
+    Split4 A[4];
+    if constexpr (SQUARE)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (rt < M.sp && ct + 16 * i < M.sp) A[i] = get_split4(ma.ws + M.a, split_at(rt, ct + 16 * i, M.sp));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float x[4];
+        if constexpr (SQUARE) values(A[i], x);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float y = sum[i][e] * kMuonUnscale;
+            x[e] = SQUARE ? ma.qb * x[e] + ma.qc * y : y;
+        }
+        store_symmetric(ma.ws + (SQUARE ? M.b : M.a), M.sp, rt, ct + 16 * i, x);
+    }
 }
 
 // X <- a X + B X or a X + X B
@@ -392,12 +473,12 @@ __global__ __launch_bounds__((Tile<W, PAIR>::kLanes), (Tile<W, PAIR>::kWavesPerS
 }  // namespace
 
 template <int W, bool PAIR>
-static void launch_gram(const StepArgs &a, const MuonArgs &ma, int64_t tiles, int32_t from, hipStream_t s) {
-    LAUNCH_TRACED((muon_gram_kernel<W, PAIR>), (unsigned)tiles, (Tile<W, PAIR>::kLanes), s, a, ma, from);
+static void launch_gram(const StepArgs &a, const MuonArgs &ma, int64_t tiles, int32_t parts, int32_t from, hipStream_t s) {
+    LAUNCH_TRACED((muon_gram_kernel<W, PAIR>), dim3((unsigned)tiles, (unsigned)parts), (Tile<W, PAIR>::kLanes), s, a, ma, from);
 }
 template <int W, bool PAIR>
-static void launch_square(const StepArgs &a, const MuonArgs &ma, int64_t tiles, hipStream_t s) {
-    LAUNCH_TRACED((muon_square_kernel<W, PAIR>), (unsigned)tiles, (Tile<W, PAIR>::kLanes), s, a, ma);
+static void launch_square(const StepArgs &a, const MuonArgs &ma, int64_t tiles, int32_t parts, hipStream_t s) {
+    LAUNCH_TRACED((muon_square_kernel<W, PAIR>), dim3((unsigned)tiles, (unsigned)parts), (Tile<W, PAIR>::kLanes), s, a, ma);
 }
 
 template <int W, bool PAIR, int PK>
@@ -427,12 +508,15 @@ static void launch_iteration(const StepArgs &a, const MuonArgs &args, const Muon
     ma.full += R.full0;
     rest.sym = ma.sym + R.wide_sym;
     rest.full = ma.full + R.wide_full;
-    if (R.wide_sym) launch_gram<2, false>(a, ma, R.wide_sym, from, s);
-    if (R.nsym && R.pair_sym) launch_gram<1, true>(a, rest, R.nsym, from, s);
-    else if (R.nsym) launch_gram<1, false>(a, rest, R.nsym, from, s);
-    if (R.wide_sym) launch_square<2, false>(a, ma, R.wide_sym, s);
-    if (R.nsym && R.pair_sym) launch_square<1, true>(a, rest, R.nsym, s);
-    else if (R.nsym) launch_square<1, false>(a, rest, R.nsym, s);
+    if (R.wide_sym) launch_gram<2, false>(a, ma, R.wide_sym, 1, from, s);
+    if (R.nsym && R.pair_sym) launch_gram<1, true>(a, rest, R.nsym, R.most_parts[0], from, s);
+    else if (R.nsym) launch_gram<1, false>(a, rest, R.nsym, R.most_parts[0], from, s);
+    const dim3 quarters((unsigned)R.nsym, 4);
+    if (R.most_parts[0] > 1) LAUNCH_TRACED((muon_join_kernel<false>), quarters, kThreads, s, a, rest);
+    if (R.wide_sym) launch_square<2, false>(a, ma, R.wide_sym, 1, s);
+    if (R.nsym && R.pair_sym) launch_square<1, true>(a, rest, R.nsym, R.most_parts[1], s);
+    else if (R.nsym) launch_square<1, false>(a, rest, R.nsym, R.most_parts[1], s);
+    if (R.most_parts[1] > 1) LAUNCH_TRACED((muon_join_kernel<true>), quarters, kThreads, s, a, rest);
     StepArgs b = a;
     b.commit = commit && !R.nfull;  // the last launch publishes the step
     if (R.wide_full) launch_apply<2, false>(b, ma, R.wide_full, from, pk, s);

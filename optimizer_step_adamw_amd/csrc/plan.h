@@ -222,9 +222,17 @@ constexpr int64_t kMuonUnit = 4096;  // elements of padded X per workgroup of th
 constexpr int32_t kMuonSlab = 16384;
 constexpr int64_t kMuonMaxSlabs = 128;
 constexpr int64_t kMuonWideMin = 512;  // shorter side of matrices that may take wide tiles
+// Tiles of A and of A A are summed in pieces where few workgroups would have
+// long sums: a piece is of the steps (of 32) that would share all tiles' steps
+// out to the compute units, at least kMuonPieceMin, and only if the longest sum
+// is kMuonPieceGain steps longer.  The pieces are joined by a launch of their
+// own.  Measured, A whole and in pieces with the joining: 640 x 640 22.8 and
+// 17.7 us (20 steps, 2 pieces), 1024 x 1024 27.5 and 18.2, 3981 x 136 66.4 and
+// 22.1.
+constexpr int64_t kMuonPieceMin = 8, kMuonPieceGain = 12;
 constexpr int64_t kMuonMaxSide = int64_t(1) << 20;
 constexpr int64_t kMuonRunBytes = int64_t(4) << 30;  // workspace of one run of launches
-struct MuonMat {          // 80 bytes
+struct MuonMat {          // 96 bytes
     int64_t elem0;        // its first element in the tensor
     int64_t x[2], a, b;   // X (read and written in turn), A, B
     int64_t unit0;        // first unit of the splitting pass, within its run
@@ -234,8 +242,10 @@ struct MuonMat {          // 80 bytes
     int32_t sp;           // padded shorter side
     int32_t tall;         // rows > cols
     int32_t slabs;        // of a matrix with a short side (sp 64 or 128)
+    int64_t part;         // partial sums of A, then of A A
+    int32_t parts[2];     // pieces that tiles of A and of A A are summed in
 };
-static_assert(sizeof(MuonMat) == 80, "MuonMat layout");
+static_assert(sizeof(MuonMat) == 96, "MuonMat layout");
 struct MuonTile {         // 8 bytes
     int32_t mat;
     uint16_t i, j;        // tile row and column
@@ -255,6 +265,7 @@ struct MuonRun {          // matrices [mat0, mat1) that share a run of launches
     int32_t wide;         // wide tiles
     int32_t pair_sym, pair_full;  // the others by two groups of wavefronts each
     int32_t most_slabs;   // of one matrix
+    int32_t most_parts[2];  // of one matrix
 };
 
 // Workspace layout (byte offsets from the workspace base, 256-aligned).
