@@ -215,22 +215,22 @@ __device__ __forceinline__ void load_p(const D &T, int64_t e, float (&p)[N]) {
     }
 }
 
-template <int PK, int N, int LAY = kStrided, class D>
+template <int PK, int N, class D>
 __device__ __forceinline__ void store_p(const D &T, int64_t e, const float (&p)[N]) {
     if constexpr (PK == P_F32) {
-        stf<N, LAY>(static_cast<float *>(T.p), e, p);
+        stf<N>(static_cast<float *>(T.p), e, p);
     } else if constexpr (PK == P_BF16R) {
         uint32_t b[N], r[N];
 #pragma unroll
         for (int k = 0; k < N; ++k) rem_split(p[k], b[k], r[k]);
-        sth<N, LAY>(static_cast<uint16_t *>(T.p), e, b);
-        sth<N, LAY>(T.rem, e, r);
+        sth<N>(static_cast<uint16_t *>(T.p), e, b);
+        sth<N>(T.rem, e, r);
     } else {
-        stf<N, LAY>(T.master, e, p);
+        stf<N>(T.master, e, p);
         uint32_t c[N];
 #pragma unroll
         for (int k = 0; k < N; ++k) c[k] = PK == P_MBF16 ? f32_to_bf16_rne(p[k]) : f32_to_f16_rne(p[k]);
-        sth<N, LAY>(static_cast<uint16_t *>(T.p), e, c);
+        sth<N>(static_cast<uint16_t *>(T.p), e, c);
     }
 }
 
@@ -475,30 +475,17 @@ __device__ __forceinline__ uint32_t arrive(uint32_t *c) {
 
 // Called by thread 0 of every workgroup; true in the last one to arrive
 // (the counters are rearmed by then).
-__device__ __forceinline__ bool last_arrival(uint32_t *done) {
+__device__ __forceinline__ bool last_arrival(const StepArgs &a) {
     const uint32_t G = gridDim.x, b = blockIdx.x;
     const uint32_t nsub = G < (uint32_t)kSubCounters ? G : (uint32_t)kSubCounters;
     const uint32_t j = b % nsub;
     const uint32_t members = G / nsub + (j < G % nsub ? 1u : 0u);
-    uint32_t *sub = done + (1 + j) * kCounterStride;
+    uint32_t *sub = a.done + (1 + j) * kCounterStride;
     if (arrive(sub) != members - 1) return false;
     __hip_atomic_store(sub, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if (arrive(done) != nsub - 1) return false;
-    __hip_atomic_store(done, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (arrive(a.done) != nsub - 1) return false;
+    __hip_atomic_store(a.done, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     return true;
-}
-__device__ __forceinline__ bool last_arrival(const StepArgs &a) { return last_arrival(a.done); }
-
-// A value that another workgroup of the same launch reads: stored and loaded
-// at device scope, past the XCD's own L2.  The writer waits here for its
-// store, so an arrival (arrive()) of its workgroup after that means it is
-// there; the reader loads after it has seen the arrival.
-__device__ __forceinline__ void publish(double *p, double x) {
-    __hip_atomic_store(p, x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-}
-__device__ __forceinline__ double published(const double *p) {
-    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 __device__ __forceinline__ void publish_step(const StepArgs &a, const Scalars &S) {
@@ -773,12 +760,11 @@ inline bool keep_for_second_pass(const StepArgs &a, int64_t reread_bytes_per_ele
 // trace the kernel's own start and end stamp the trace's next event pair.
 #define LAUNCH_TRACED(K, grid, block, s, ...)                                                      \
     do {                                                                                           \
-        const dim3 g_(grid);                                                                       \
-        TraceRec *tr_ = trace_slot(#K, (int64_t)g_.x * g_.y);                                      \
+        TraceRec *tr_ = trace_slot(#K, (int64_t)(grid));                                           \
         if (tr_)                                                                                   \
-            hipExtLaunchKernelGGL(K, g_, dim3(block), 0, s, tr_->start, tr_->stop, 0, __VA_ARGS__);    \
+            hipExtLaunchKernelGGL(K, dim3(grid), dim3(block), 0, s, tr_->start, tr_->stop, 0, __VA_ARGS__); \
         else                                                                                       \
-            hipLaunchKernelGGL(K, g_, dim3(block), 0, s, __VA_ARGS__);                             \
+            hipLaunchKernelGGL(K, dim3(grid), dim3(block), 0, s, __VA_ARGS__);                    \
     } while (0)
 
 #define LAUNCH_PERSISTENT(K, a, s) LAUNCH_TRACED(K, persistent_grid(K, a), kThreads, s, a)

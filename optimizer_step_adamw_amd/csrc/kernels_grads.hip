@@ -190,6 +190,18 @@ __device__ __forceinline__ double block_join(double x, double *red) {
     return t;
 }
 
+// A value that another workgroup of the same launch reads: stored and loaded
+// at device scope, past the XCD's own L2.  The writer waits here for its
+// store, so an arrival (arrive()) of its workgroup after that means it is
+// there; the reader loads after it has seen the arrival.
+__device__ __forceinline__ void publish(double *p, double x) {
+    __hip_atomic_store(p, x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+__device__ __forceinline__ double published(const double *p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
 // body(i, value) for this thread's share of n published values, 8 loads under
 // way at a time: each goes to memory past the caches (6000 vectors took 19.8 us
 // with one load at a time and the tables behind one more index, 9.6 so).
@@ -285,7 +297,11 @@ __global__ __launch_bounds__(kThreads) void grad_norms_kernel(GradArgs a, const 
         }
     }
     __syncthreads();  // every wave's sums are out before thread 0 arrives
-    if (threadIdx.x == 0) last = last_arrival(a.done);
+    if (threadIdx.x == 0) {
+        StepArgs step;
+        step.done = a.done;  // all that an arrival looks at
+        last = last_arrival(step);
+    }
     __syncthreads();
     if (!last) return;
     const double s = inv_scale ? (double)*inv_scale : 1.0;

@@ -219,10 +219,10 @@ __device__ __forceinline__ void store_piece(float *at, const Sums<1> &s) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) *(GMEM f32x4 *)(q + 16 * j * kMuonTile + 16 * i) = s.v[i][j];
 }
-// Steps of piece blockIdx.y of `parts` of a sum of `all`, and where it begins.
-__device__ __forceinline__ int piece_steps(int all, int parts, int &first) {
+// Steps of piece `part` of `parts` of a sum of `all`, and where it begins.
+__device__ __forceinline__ int piece_steps(int all, int parts, int part, int &first) {
     const int each = (all + parts - 1) / parts;
-    first = (int)blockIdx.y * each;
+    first = part * each;
     return all - first < each ? all - first : each;
 }
 
@@ -231,14 +231,15 @@ template <int W, bool PAIR>
 __global__ __launch_bounds__((Tile<W, PAIR>::kLanes), (Tile<W, PAIR>::kWavesPerSimd)) void muon_gram_kernel(StepArgs a, MuonArgs ma, int32_t from) {
     __shared__ __align__(1024) char lds[Tile<W, PAIR>::kLds];
     if (skipped(a)) return;
-    const MuonTile t = ma.sym[blockIdx.x];
+    const MuonTile t = ma.sym[blockIdx.x % ma.tiles];
     if (t.mat < 0) return;
     const MuonMat M = ma.mats[t.mat];
-    if ((int)blockIdx.y >= M.parts[0]) return;
+    const int part = blockIdx.x / ma.tiles;
+    if (part >= M.parts[0]) return;
     const char *X = ma.ws + (from ? M.x[1] : M.x[0]);
     const int64_t rows32 = split_rows32(M.ld), step = M.tall ? rows32 : kSplitBlock;
     int first;
-    const int steps = piece_steps(((M.tall ? M.rows : M.cols) + 31) / 32, M.parts[0], first);
+    const int steps = piece_steps(((M.tall ? M.rows : M.cols) + 31) / 32, M.parts[0], part, first);
     X += first * step;
     Sums<W> s{};
     if (M.tall)
@@ -250,7 +251,7 @@ __global__ __launch_bounds__((Tile<W, PAIR>::kLanes), (Tile<W, PAIR>::kWavesPerS
     join_pair<W, PAIR>(lds_at(lds), s);
     const int r0 = row0<W, PAIR>(), c0 = col0<W>();
     if constexpr (W == 1)
-        if (M.parts[0] > 1) return store_piece<PAIR>(piece_sums(ma, M, t, blockIdx.y), s);
+        if (M.parts[0] > 1) return store_piece<PAIR>(piece_sums(ma, M, t, part), s);
 #pragma unroll
     for (int j = 0; j < Tile<W, PAIR>::kOutJ; ++j)
 #pragma unroll
@@ -267,21 +268,22 @@ template <int W, bool PAIR>
 __global__ __launch_bounds__((Tile<W, PAIR>::kLanes), (Tile<W, PAIR>::kWavesPerSimd)) void muon_square_kernel(StepArgs a, MuonArgs ma) {
     __shared__ __align__(1024) char lds[Tile<W, PAIR>::kLds];
     if (skipped(a)) return;
-    const MuonTile t = ma.sym[blockIdx.x];
+    const MuonTile t = ma.sym[blockIdx.x % ma.tiles];
     if (t.mat < 0) return;
     const MuonMat M = ma.mats[t.mat];
-    if ((int)blockIdx.y >= M.parts[1]) return;
+    const int part = blockIdx.x / ma.tiles;
+    if (part >= M.parts[1]) return;
     const char *A = ma.ws + M.a;
     const int64_t rows32 = split_rows32(M.sp);
     int first;
-    const int steps = piece_steps(((M.tall ? M.cols : M.rows) + 31) / 32, M.parts[1], first);
+    const int steps = piece_steps(((M.tall ? M.cols : M.rows) + 31) / 32, M.parts[1], part, first);
     const char *P = A + first * kSplitBlock;
     Sums<W> s{};
     product<W, PAIR, KC, KC, true, false>(row_feed<W>(P, t.i, rows32, M.sp), kSplitBlock,
                                           row_feed<W>(P, t.j, rows32, M.sp), kSplitBlock, steps, lds_at(lds), s);
     join_pair<W, PAIR>(lds_at(lds), s);
     if constexpr (W == 1)
-        if (M.parts[1] > 1) return store_piece<PAIR>(piece_sums(ma, M, t, blockIdx.y), s);
+        if (M.parts[1] > 1) return store_piece<PAIR>(piece_sums(ma, M, t, part), s);
     struct Row {
         Split4 v[4];
     };
@@ -309,13 +311,13 @@ __global__ __launch_bounds__((Tile<W, PAIR>::kLanes), (Tile<W, PAIR>::kWavesPerS
 template <bool SQUARE>
 __global__ __launch_bounds__(kThreads) void muon_join_kernel(StepArgs a, MuonArgs ma) {
     if (skipped(a)) return;
-    const MuonTile t = ma.sym[blockIdx.x];
+    const MuonTile t = ma.sym[blockIdx.x % ma.tiles];
     if (t.mat < 0) return;
     const MuonMat M = ma.mats[t.mat];
     const int parts = M.parts[SQUARE];
     if (parts <= 1) return;
     const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int r = blockIdx.y * 32 + (w & 1) * 16 + (lane & 15), c = (w >> 1) * 64 + (lane >> 4) * 4;
+    const int r = (int)(blockIdx.x / ma.tiles) * 32 + (w & 1) * 16 + (lane & 15), c = (w >> 1) * 64 + (lane >> 4) * 4;
     const int64_t apart = piece_sums(ma, M, MuonTile{}, 1) - piece_sums(ma, M, MuonTile{}, 0);
     const GMEM float *q = gp(piece_sums(ma, M, t, 0)) + r * kMuonTile + c;
     f32x4 sum[4] = {};
@@ -457,7 +459,7 @@ __global__ __launch_bounds__((Tile<W, PAIR>::kLanes), (Tile<W, PAIR>::kWavesPerS
                     p[e] = decayed(b.p[i][e], lw, f * x[e]);
                 }
                 if (vec && left(i, j) >= 4) {
-                    store_p<PK, 4, kStridedKeep>(T, at(i, j), p);
+                    store_p_keep<PK, 4>(T, at(i, j), p);
                 } else {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
@@ -474,11 +476,11 @@ __global__ __launch_bounds__((Tile<W, PAIR>::kLanes), (Tile<W, PAIR>::kWavesPerS
 
 template <int W, bool PAIR>
 static void launch_gram(const StepArgs &a, const MuonArgs &ma, int64_t tiles, int32_t parts, int32_t from, hipStream_t s) {
-    LAUNCH_TRACED((muon_gram_kernel<W, PAIR>), dim3((unsigned)tiles, (unsigned)parts), (Tile<W, PAIR>::kLanes), s, a, ma, from);
+    LAUNCH_TRACED((muon_gram_kernel<W, PAIR>), (unsigned)(tiles * parts), (Tile<W, PAIR>::kLanes), s, a, ma, from);
 }
 template <int W, bool PAIR>
 static void launch_square(const StepArgs &a, const MuonArgs &ma, int64_t tiles, int32_t parts, hipStream_t s) {
-    LAUNCH_TRACED((muon_square_kernel<W, PAIR>), dim3((unsigned)tiles, (unsigned)parts), (Tile<W, PAIR>::kLanes), s, a, ma);
+    LAUNCH_TRACED((muon_square_kernel<W, PAIR>), (unsigned)(tiles * parts), (Tile<W, PAIR>::kLanes), s, a, ma);
 }
 
 template <int W, bool PAIR, int PK>
@@ -508,10 +510,12 @@ static void launch_iteration(const StepArgs &a, const MuonArgs &args, const Muon
     ma.full += R.full0;
     rest.sym = ma.sym + R.wide_sym;
     rest.full = ma.full + R.wide_full;
+    ma.tiles = (int32_t)R.wide_sym;
+    rest.tiles = (int32_t)R.nsym;
     if (R.wide_sym) launch_gram<2, false>(a, ma, R.wide_sym, 1, from, s);
     if (R.nsym && R.pair_sym) launch_gram<1, true>(a, rest, R.nsym, R.most_parts[0], from, s);
     else if (R.nsym) launch_gram<1, false>(a, rest, R.nsym, R.most_parts[0], from, s);
-    const dim3 quarters((unsigned)R.nsym, 4);
+    const unsigned quarters = (unsigned)R.nsym * 4;
     if (R.most_parts[0] > 1) LAUNCH_TRACED((muon_join_kernel<false>), quarters, kThreads, s, a, rest);
     if (R.wide_sym) launch_square<2, false>(a, ma, R.wide_sym, 1, s);
     if (R.nsym && R.pair_sym) launch_square<1, true>(a, rest, R.nsym, R.most_parts[1], s);

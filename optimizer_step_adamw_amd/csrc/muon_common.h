@@ -52,5 +52,24 @@ __device__ __forceinline__ double muon_factor(double sum, double eps) {
     return n == 0.0 ? 0.0 : (double)kMuonScale / n;
 }
 
+// A parameter's stores with ordinary accesses: a tile's rows are 64-byte runs,
+// which non-temporal stores would write one by one.
+template <int PK, int N>
+__device__ __forceinline__ void store_p_keep(const TensorDesc &T, int64_t e, const float (&p)[N]) {
+    if constexpr (PK == P_F32) {
+        stf<N, kStridedKeep>(static_cast<float *>(T.p), e, p);
+    } else {
+        uint32_t b[N], r[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            if constexpr (PK == P_BF16R) rem_split(p[k], b[k], r[k]);
+            else b[k] = PK == P_MBF16 ? f32_to_bf16_rne(p[k]) : f32_to_f16_rne(p[k]);
+        }
+        sth<N, kStridedKeep>(static_cast<uint16_t *>(T.p), e, b);
+        if constexpr (PK == P_BF16R) sth<N, kStridedKeep>(T.rem, e, r);
+        else stf<N, kStridedKeep>(T.master, e, p);
+    }
+}
+
 }  // namespace
 }  // namespace optim

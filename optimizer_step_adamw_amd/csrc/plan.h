@@ -406,6 +406,7 @@ struct MuonArgs {
     const MuonTile *sym, *full;
     char *ws;             // the region the runs share
     int32_t mat0, mat1;   // this run's matrices
+    int32_t tiles;        // of the symmetric products, per piece
     float qa, qb, qc;     // the quintic
     int32_t scale_kind;
     // matrices of one slab: [lone0, nmats), the first lone_narrow of them of
