@@ -32,7 +32,8 @@ extern "C" {
  * depend on it.  grid, state_dtype and state_layout must be 0.
  * The workspace holds, for every matrix of the largest run, about 8 bytes an
  * element and 8 bytes times the square of its shorter side, sides rounded up
- * to 32.
+ * to 32 (with a side of at most 128: up to 12 bytes an element, that side
+ * rounded up to 64 or 128), and up to 64 MB beside.
  * optim_check_finite, optim_grad_norm, optim_plan_set_schedule and
  * optim_plan_trace take such a plan as any other.                          */
 

@@ -334,10 +334,11 @@ int64_t muon_slabs(int64_t rows, int64_t cols) {
     return (std::max(rows, cols) + l - 1) / l;
 }
 
-MuonKind muon_kind(int64_t rows, int64_t cols, bool wide) {
+MuonKind muon_kind(int64_t rows, int64_t cols, bool wide, bool slabs128) {
     const int64_t s = std::min(rows, cols), p = muon_slabs(rows, cols);
     if (s <= 128 && p == 1) return s <= 64 ? kLone64 : kLone128;
-    if (s <= 128 && p <= kMuonMaxSlabs) return s <= 64 ? kSlabs64 : kSlabs128;
+    if (s <= 64 && p <= kMuonMaxSlabs) return kSlabs64;
+    if (s <= 128 && p <= kMuonMaxSlabs && slabs128) return kSlabs128;
     return wide && wide_matrix(rows, cols) ? kWide : kTiles;
 }
 
@@ -419,22 +420,24 @@ int add_matrices(const std::string &ti, int i, int64_t numel, int64_t rows, int6
 
 // Muon: the matrices of the list, kind by kind, so that a run's are of one
 // kind; wide tiles where all matrices that may take them make a round of the
-// GPU.
+// GPU, slabs of the wider kind where all of them are few.
 int add_muon(const optim_tensor_list *list, int64_t cap, Built &B) {
-    int64_t wide_full = 0;
+    int64_t wide_full = 0, slabs128 = 0;
     for (int i = 0; i < list->n; ++i) {
         if (list->numel[i] == 0) continue;
         const int64_t r = list->rows[i], c = list->cols[i];
         if (r < 1 || c < 1 || r > kMuonMaxSide || c > kMuonMaxSide)
             return fail(OPTIM_EINVAL, "tensor " + std::to_string(i) + ": rows and cols must be in [1, 2^20]");
-        if (muon_kind(r, c, true) == kWide)
+        const MuonKind kind = muon_kind(r, c, true, true);
+        if (kind == kSlabs128) slabs128 += std::min(list->numel[i] / (r * c), kMuonSlabRoom + 1) * muon_slabs(r, c);
+        if (kind == kWide)
             wide_full += list->numel[i] / (r * c) * count_of(r, kMuonWideTile) * count_of(c, kMuonWideTile);
     }
     for (int kind = 0; kind < kMuonKinds; ++kind)
         for (int i = 0; i < list->n; ++i) {
             if (list->numel[i] == 0) continue;
             const int64_t r = list->rows[i], c = list->cols[i];
-            if (muon_kind(r, c, wide_full >= kMuonSlots) != kind) continue;
+            if (muon_kind(r, c, wide_full >= kMuonSlots, slabs128 <= kMuonSlabRoom) != kind) continue;
             if (const int rc = add_matrices("tensor " + std::to_string(i) + ": ", i, list->numel[i], r, c, (MuonKind)kind,
                                             cap, B))
                 return rc;

@@ -8,6 +8,11 @@
 // latencies away.  Only one array is walked, so any alignment takes the
 // vector path: the elements before the first 16-byte boundary and behind the
 // last one go one by one.
+//
+// Measured on MI355X: norms of 1.1B bf16 372 us (6.1 TB/s; 4 or 16 loads
+// of 16 bytes a lane under way instead of 8 are within 2%); norms and clip of
+// 667M bf16 569 us (4.0 GB moved, 7.0 TB/s with what the Infinity Cache holds),
+// of 4096 x 4096 fp32 38 us; norms of 6000 vectors 9.6 us.
 #include "optim_grads.h"
 
 #include "device_common.h"

@@ -13,6 +13,16 @@
 // One launch of a kernel covers the tiles of every matrix of a run, from a
 // table of (matrix, tile row, tile column).  Matrices with a side of at most
 // 128 go another way (kernels_muon_slab.hip).
+//
+// Measured on MI355X, a step of five iterations: the seven matrices of a
+// 4096-wide layer (202M elements, 14.8 TFLOP with symmetric products counted
+// once, three times that on the matrix cores) 36.2 ms, of it products 35.1 ms at
+// 1260 TFLOP/s of fp16 products, the matrix cores busy 68-75% of the time at the
+// clock that the power limit leaves (1.83 GHz); momentum 0.38 ms (2.4 GB, 6.4
+// TB/s), first split 0.46 ms (2.4 GB).  48 matrices of 1000 x 408: 1.06-1.09 ms,
+// the matrix cores busy 25-52%: X passes through the Infinity Cache in
+// every product (79 MB read and 79 MB written in 93 us), and 13 to 32 steps a
+// tile do not hide a tile's beginning and end.
 #include "muon_common.h"
 
 namespace optim {

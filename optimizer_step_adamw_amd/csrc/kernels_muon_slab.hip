@@ -9,9 +9,13 @@
 // matrix of one slab needs no passing at all: momentum, norm, all iterations
 // and the update are one launch.
 //
-// What bounds it is latency (an iteration is a few microseconds of dependent
-// LDS reads, products and barriers).  Measured on MI355X: see the table of the
-// launches at their kernels.
+// What bounds it is latency: an iteration is a chain of LDS reads, products and
+// barriers, 5 us for SP 64 and 12 us for SP 128, whatever the number of
+// matrices up to one per compute unit.  Measured on MI355X, the whole step of
+// five iterations: one 64 x 64 37 us, 14 of 64 x 172 54 us, 500 of 64 x 64
+// 80 us, one 128 x 128 91 us (by tiles and launches per product 190 us and
+// more); in several slabs 20 of 3591 x 21 151 us (by tiles 542), one
+// 128 x 1024 151 us, one of 128 slabs (1 x 16384 x 128) 228 us (1353).
 //
 // X lies in LDS as rows of positions along the long side, 32 values along the
 // short side to a 128-byte row (32 high parts, 32 low parts; chunks of 16
@@ -430,9 +434,13 @@ __global__ __launch_bounds__(kThreads) void muon_slab_first_kernel(StepArgs a, M
     slab_save_part<SP>(slab_part<SP>(ma, M, 0, t.i), A);
 }
 
-// Matrices of more than kSlabJoin slabs have their parts summed by a launch of
-// their own, into the first part; else every slab sums them itself.
-constexpr int32_t kSlabJoin = 4;
+// Matrices with more slabs than this have their parts of A summed by a launch of
+// their own, into the first part; else every slab sums them itself.  Measured,
+// by itself and by a launch: one 128 x 256 (2 slabs) 146 and 162 us, 128 x 512
+// (4) 181 and 164, 128 x 1024 (8) 251 and 151; one 64 x 1024 (4) 99 and 109,
+// 64 x 2048 (8) 109 and 108.
+template <int SP>
+constexpr int32_t kSlabJoin = SP == 64 ? 8 : 3;
 
 // One iteration: X and the parts of A (set `set`) in, X and its part of the
 // next A (the other set) out, or the update (PK >= 0).
@@ -451,7 +459,7 @@ __global__ __launch_bounds__(kThreads) void muon_slab_kernel(StepArgs a, MuonArg
         for (int k = 0; k < kMuonSlab / 4 / kThreads; ++k) x[k] = ((const GMEM u32x4 *)gp(image))[k * kThreads + threadIdx.x];
         Square<SP> A{};
         const float *part = slab_part<SP>(ma, M, set, 0);
-        const int32_t parts = M.slabs > kSlabJoin ? 1 : M.slabs;
+        const int32_t parts = M.slabs > kSlabJoin<SP> ? 1 : M.slabs;
 #pragma unroll 2
         for (int32_t k = 0; k < parts; ++k, part += SP * SP)
 #pragma unroll
@@ -489,7 +497,7 @@ __global__ __launch_bounds__(kThreads) void muon_slab_join_kernel(StepArgs a, Mu
     if (skipped(a)) return;
     const MuonTile t = ma.full[blockIdx.x];
     const MuonMat M = ma.mats[t.mat];
-    if (M.slabs <= kSlabJoin) return;
+    if (M.slabs <= kSlabJoin<SP>) return;
     for (int32_t q = t.i * kThreads + threadIdx.x; q < SP * SP / 4; q += M.slabs * kThreads) {
         float *part = slab_part<SP>(ma, M, set, 0) + q * 4;
         f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -568,9 +576,9 @@ hipError_t launch_muon_slabs(const StepArgs &a, const MuonArgs &args, const Muon
     MuonArgs ma = args;
     ma.full += R.full0;
     const int64_t rest = R.slabs - R.narrow;
-    launch_slabs_of<64>(a, ma, R.narrow, R.most_slabs > kSlabJoin, pk, gk, steps, nesterov, commit && rest == 0, s);
+    launch_slabs_of<64>(a, ma, R.narrow, R.most_slabs > kSlabJoin<64>, pk, gk, steps, nesterov, commit && rest == 0, s);
     ma.full += R.narrow;
-    launch_slabs_of<128>(a, ma, rest, R.most_slabs > kSlabJoin, pk, gk, steps, nesterov, commit, s);
+    launch_slabs_of<128>(a, ma, rest, R.most_slabs > kSlabJoin<128>, pk, gk, steps, nesterov, commit, s);
     return hipGetLastError();
 }
 

@@ -218,10 +218,17 @@ constexpr int64_t kMuonUnit = 4096;  // elements of padded X per workgroup of th
 // (positions along the longer side times the shorter side padded to 64 or 128)
 // that a workgroup holds in LDS.  A matrix of one slab has its whole step in
 // one launch; of several (up to kMuonMaxSlabs), their parts of A pass
-// through the workspace.
+// through the workspace; unless a plan has more than kMuonSlabRoom slabs of the
+// wider kind in such matrices, which then fill the GPU by tiles.  Measured,
+// by slabs and by tiles: one 128 x 8192 (64 slabs) 176 and 308 us, 128 x 65536
+// (512) 444 and 644, 4 of 128 x 16384 (512) 367 and 481, 64 of 128 x 2048
+// (1024) 652 and 530, 16 of 128 x 16384 (2048) 1390 and 926; 64 x 131072 (512)
+// 330 and 947, 256 of 64 x 2048 (2048) 847 and 981.
 constexpr int32_t kMuonSlab = 16384;
-constexpr int64_t kMuonMaxSlabs = 128;
-constexpr int64_t kMuonWideMin = 512;  // shorter side of matrices that may take wide tiles
+constexpr int64_t kMuonMaxSlabs = 512, kMuonSlabRoom = 768;
+// Shorter side of matrices that may take wide tiles (from 400 on, 48 matrices
+// of 1000 x 408 took 1267 us instead of 1131).
+constexpr int64_t kMuonWideMin = 512;
 // Tiles of A and of A A are summed in pieces where few workgroups would have
 // long sums: a piece is of the steps (of 32) that would share all tiles' steps
 // out to the compute units, at least kMuonPieceMin, and only if the longest sum

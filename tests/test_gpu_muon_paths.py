@@ -24,7 +24,10 @@ LISTS = {
     "pieces": [(1, 1500, 140), (2, 401, 900), (1, 160, 160)],
     "pieces of both": [(1, 900, 1040), (1, 700, 650)],
     "slabs": [(1, 64, 5000), (3, 2100, 33), (1, 100, 2000), (2, 1300, 128), (1, 1, 20000)],
-    "most slabs": [(1, 17, 32768), (1, 16384, 65), (1, 32769, 20)],
+    "most slabs": [(1, 17, 32768), (1, 16384, 65), (1, 32769, 20), (1, 131072, 40)],
+    # one slab too many for a matrix, and too many in all
+    "past the slabs": [(1, 65537, 70), (1, 131073, 5)],
+    "many slabs": [(97, 128, 1000), (2, 64, 700)],
 }
 
 
