@@ -92,7 +92,8 @@ int optim_clip_grads(optim_plan *plan, const float *coef_dev,
  * optim_expert_grad_workspace bytes, contents free between calls); NULL
  * sums in one piece, too few bytes are OPTIM_EWORKSPACE.  Either way the order of
  * sums is fixed by the sizes: results repeat bit for bit.
- * experts, tokens < 2^31; m, n < 2^24; ldx >= m, ldy >= n.  dW must not
+ * tokens < 2^31; m, n < 2^24; fewer than 2^18 blocks of 512 x 512 over all
+ * experts (an expert is at least one); ldx >= m, ldy >= n.  dW must not
  * overlap X, dY or the workspace.  16-byte aligned X and dY with m, n, ldx
  * and ldy multiples of 8 take the fastest path.                            */
 int optim_expert_grad_workspace(int32_t experts, int64_t tokens, int64_t m,

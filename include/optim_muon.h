@@ -26,7 +26,7 @@ extern "C" {
  * BF16 or F16 with master).  Tensor i holds numel / (rows * cols) matrices
  * of rows x cols each, row by row, one after another (the weights of a
  * layer's experts are one tensor); rows, cols in [1, 2^20], and numel must
- * be a multiple of rows * cols (0: skipped).
+ * be a multiple of rows * cols (0: skipped).  Fewer than 2^23 matrices in all.
  * opts: segment_bytes bounds the workspace that the matrices of one run of
  * launches take (0 = 4 GiB; a larger matrix has a run alone); results do not
  * depend on it.  grid, state_dtype and state_layout must be 0.

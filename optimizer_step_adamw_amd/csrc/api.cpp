@@ -360,7 +360,7 @@ int add_matrices(const std::string &ti, int i, int64_t numel, int64_t rows, int6
     const int64_t bytes = (slabs ? 1 : 2) * xbytes + 2 * abytes;
     const int64_t nt = count_of(sp, tile);
     const int64_t tiles = slabs ? p : nt * (nt + 1) / 2 + count_of(rp, tile) * count_of(ld, tile);
-    if (count > INT32_MAX / 4 || (int64_t)B.mats.size() + count > ((int64_t)1 << 26) ||
+    if (count > INT32_MAX / 4 || (int64_t)B.mats.size() + count >= ((int64_t)1 << 23) ||
         tiles > (((int64_t)1 << 26) - B.muon_tiles) / count)
         return fail(OPTIM_EUNSUPPORTED, ti + "too many matrices or tiles");
     B.muon_tiles += tiles * count;
@@ -475,6 +475,7 @@ int build_grads(const optim_tensor_list *list, const optim_plan_opts *opts, Buil
     }
     int64_t item = kGradItemMax;
     while (item > kGradItemMin && B.gbytes < item * kGradItems) item /= 2;
+    while (B.gbytes / item >= kGradMostItems / 2) item *= 2;
     item /= (int64_t)gsz;  // elements
     for (int i = 0; i < n; ++i) {
         const int64_t numel = list->numel[i];
@@ -485,7 +486,7 @@ int build_grads(const optim_tensor_list *list, const optim_plan_opts *opts, Buil
             continue;
         }
         const int64_t items = (numel + item - 1) / item;
-        if (items + (int64_t)B.gitems.size() + n >= INT32_MAX) return fail(OPTIM_EUNSUPPORTED, "gradient list too long");
+        if (items + (int64_t)B.gitems.size() >= kGradMostItems) return fail(OPTIM_EUNSUPPORTED, "too many gradients in one list");
         for (int64_t k = 0; k < items; ++k)
             B.gitems.push_back(GradItem{g + k * item * (int64_t)gsz, B.npartials, i,
                                         (int32_t)std::min(item, numel - k * item), (int32_t)k, (int32_t)items});
@@ -494,6 +495,8 @@ int build_grads(const optim_tensor_list *list, const optim_plan_opts *opts, Buil
     int64_t kept = 0;
     B.gkeep0 = (int32_t)B.gitems.size();
     while (B.gkeep0 > 0 && kept < kGradKeepBytes) kept += B.gitems[--B.gkeep0].len * (int64_t)gsz;
+    if ((int64_t)(B.gitems.size() + B.gsmall.size() / 4 + 1) >= kGradMostItems)
+        return fail(OPTIM_EUNSUPPORTED, "too many gradients in one list");
     if (const int rc = check_overlaps(ranges)) return rc;
 
     Layout &L = B.L;
@@ -1346,10 +1349,10 @@ int check_expert_sizes(int32_t experts, int64_t tokens, int64_t m, int64_t n) {
     if (experts < 0 || tokens < 0 || m < 0 || n < 0) return fail(OPTIM_EINVAL, "negative size");
     if (tokens > INT32_MAX) return fail(OPTIM_EINVAL, "tokens must be below 2^31");
     if (m > kExpertMaxSide || n > kExpertMaxSide) return fail(OPTIM_EINVAL, "m and n must be below 2^24");
-    // tiles are counted in 32 bits, elements of dW in 48
-    const int64_t tiles = ((m + 127) / 128) * ((n + 127) / 128);
-    if (experts > 0 && (tiles > (int64_t(1) << 26) / experts || (m > 0 && n > kMaxNumel / m / experts)))
-        return fail(OPTIM_EUNSUPPORTED, "dW has too many elements");
+    // a launch has fewer than 2^32 lanes: 16 tiles a block, up to 512 lanes each
+    const int64_t blocks = ((m + 511) / 512) * ((n + 511) / 512);
+    if (blocks * experts >= int64_t(1) << 18 || (experts > 0 && m > 0 && n > kMaxNumel / m / experts))
+        return fail(OPTIM_EUNSUPPORTED, "dW has too many experts or elements");
     return OPTIM_OK;
 }
 

@@ -187,6 +187,7 @@ constexpr size_t kAmaxBytesPerBlock = 2 * kAmaxSlots * kCounterStride * sizeof(u
 constexpr int64_t kGradItemMax = 256 << 10;
 constexpr int64_t kGradItemMin = 64 << 10;
 constexpr int64_t kGradItems = 256;
+constexpr int64_t kGradMostItems = int64_t(1) << 24;  // a launch has fewer than 2^32 lanes
 constexpr int64_t kGradSmall = 4096;   // elements of a small tensor at most
 // The list's last bytes are read with ordinary loads, the others non-temporal:
 // they stay in the 256 MB Infinity Cache for the clip that follows.  Measured,
