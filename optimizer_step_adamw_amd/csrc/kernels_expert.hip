@@ -32,7 +32,12 @@ constexpr int kStepRows = 64;
 constexpr int kXcds = 8, kBand = 4, kGroup = kBand * kBand;
 
 // One operand's 64 x 128 tile from row k0 on, through registers: 4 chunks of
-// 8 values per lane.
+// 8 values per lane.  With 8 rows of the run and more behind the step, 16 bytes
+// from any of its elements are the run's, and all chunks are loaded at once;
+// what of them lies past the columns becomes zero on the way to LDS.  Bounded
+// one by one, as in a run's last rows, the loads wait for each other: 2 experts
+// of 3055 x 1157 over 7334 rows took 407 us instead of 208, 8 of 1001 x 999 over
+// 8192 98 instead of 48.
 struct Chunks {
     s16x8 v[4];
 };
@@ -40,6 +45,15 @@ typedef s16x8 __attribute__((aligned(2))) s16x8_any;
 template <int W>
 __device__ __forceinline__ Chunks load_chunks(const char *src, int64_t ld, int32_t rows, int32_t cols) {
     Chunks r;
+    if (rows >= kStepRows + 8) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            int row, chunk;
+            feed_slot<W, KR, false>(t, row, chunk);
+            r.v[t] = *(const GMEM s16x8_any *)gp(src + row * ld + (chunk * 8 < cols ? chunk * 16 : 0));
+        }
+        return r;
+    }
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
         int row, chunk;
@@ -61,10 +75,18 @@ __device__ __forceinline__ Chunks load_chunks(const char *src, int64_t ld, int32
     return r;
 }
 template <int W>
-__device__ __forceinline__ void write_chunks(const Chunks &r, char *lds) {
+__device__ __forceinline__ void write_chunks(const Chunks &r, char *lds, int32_t cols) {
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
-        *(LMEM s16x8 *)(lds + (wave<W>() * 4 + t) * 1024 + (threadIdx.x & 63) * 16) = r.v[t];
+    for (int t = 0; t < 4; ++t) {
+        s16x8 v = r.v[t];
+        if (cols < Tile<W>::kSide) {
+            int row, chunk;
+            feed_slot<W, KR, false>(t, row, chunk);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = chunk * 8 + i < cols ? v[i] : (short)0;
+        }
+        *(LMEM s16x8 *)(lds + (wave<W>() * 4 + t) * 1024 + (threadIdx.x & 63) * 16) = v;
+    }
 }
 
 // Four neighbouring elements of dW, n of which exist; `vec`: they are one access.
@@ -154,8 +176,8 @@ __global__ __launch_bounds__(Tile<W>::kLanes, Tile<W>::kWavesPerSimd) void exper
     if (done < rows) {
         Chunks cx = load_chunks<W>(x + done * a.ldx, a.ldx, rows - done, mleft);
         Chunks cy = load_chunks<W>(y + done * a.ldy, a.ldy, rows - done, nleft);
-        write_chunks<W>(cx, lds);
-        write_chunks<W>(cy, lds + Tile<W>::kOperand);
+        write_chunks<W>(cx, lds, mleft);
+        write_chunks<W>(cy, lds + Tile<W>::kOperand, nleft);
         for (int32_t half = 0;; half ^= 1) {
             char *next = lds + (half ^ 1) * Tile<W>::kStage;
             const uint32_t now = lds_at(lds) + half * Tile<W>::kStage;
@@ -174,8 +196,8 @@ __global__ __launch_bounds__(Tile<W>::kLanes, Tile<W>::kWavesPerSimd) void exper
                 multiply<false, BF16, W>(q, p, s, j);
             }
             if (!more) break;
-            write_chunks<W>(cx, next);
-            write_chunks<W>(cy, next + Tile<W>::kOperand);
+            write_chunks<W>(cx, next, mleft);
+            write_chunks<W>(cy, next + Tile<W>::kOperand, nleft);
         }
     }
     const float sc = a.scale ? *a.scale : 1.0f;
@@ -268,10 +290,10 @@ hipError_t launch_expert_t(const ExpertArgs &args, bool direct, hipStream_t s) {
     ExpertArgs a = args;
     unsigned grid;
     if (!set_tiles<W>(a, grid)) return hipErrorInvalidValue;
-    if (direct)
+    if (W == 2 || direct)  // wide tiles are for whole chunks
         hipLaunchKernelGGL((expert_grad_kernel<W, BF16, F32, true>), dim3(grid), dim3(Tile<W>::kLanes), 0, s, a);
     else
-        hipLaunchKernelGGL((expert_grad_kernel<W, BF16, F32, false>), dim3(grid), dim3(Tile<W>::kLanes), 0, s, a);
+        hipLaunchKernelGGL((expert_grad_kernel<1, BF16, F32, false>), dim3(grid), dim3(Tile<1>::kLanes), 0, s, a);
     if (a.parts) {
         const int64_t quads = ((int64_t)a.experts * a.m * a.n + 3) / 4;
         const int64_t g = (quads + kThreads - 1) / kThreads;

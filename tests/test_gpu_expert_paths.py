@@ -29,6 +29,19 @@ def test_wide_tiles(m, n, dtype, out, accumulate):
         check(x, y, off, old, dw, accumulate, 0.5)
 
 
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("m,n", [(1, 1), (3, 9), (7, 300), (130, 129), (257, 15)])
+def test_odd_columns_and_ends_of_runs(m, n, out):
+    """Whole steps of odd matrices read ahead by up to 8 rows: runs that end on both sides of that, the last at the end
+    of the array, and columns, rows between and rows outside that hold NaN."""
+    runs = [71, 72, 73, 0, 135, 136, 137, 64, 8, 199, 200, 201, 72]
+    for kw in ({}, dict(before=1, behind=1), dict(padx=1, pady=5, shift=1), dict(padx=7)):
+        x, y, o, dw, off = make(runs, m, n, torch.bfloat16, out, seed=9, **kw)
+        old = dw.clone()
+        osa.optim_expert_grad(x, y, o, dw, accumulate=True)
+        check(x, y, off, old, dw, True, 1.0)
+
+
 def test_two_calls_at_once():
     cases = [make(RUNS, m, n, torch.bfloat16, torch.float32, seed=5) for m, n in SIZES[:2]]
     want = []
