@@ -17,6 +17,7 @@
 // 512 rows 11.8 us.
 #include "optim_grads.h"
 
+#include "expert_rows.h"
 #include "tiles.h"
 
 #include <algorithm>
@@ -24,7 +25,6 @@
 namespace optim {
 namespace {
 
-constexpr int kStepRows = 64;
 // Tiles are taken in blocks of kBand x kBand of one expert, each block by
 // one XCD (workgroup b runs on XCD b mod 8), whose L2 then holds the
 // block's operands, and consecutive blocks by different XCDs, so that an
@@ -134,19 +134,6 @@ __device__ __forceinline__ void dw_put(char *dw, int64_t e, int n, bool vec, f32
     }
 }
 
-// The rows of expert e's run that piece `piece` sums: whole steps of 64 but
-// for the last.
-__device__ __forceinline__ void expert_run(const ExpertArgs &a, int32_t e, int32_t piece, int32_t &k0, int32_t &k1) {
-    int32_t b = a.offsets[e], c = a.offsets[e + 1];
-    b = b < 0 ? 0 : (b < a.tokens ? b : a.tokens);
-    c = c < b ? b : (c < a.tokens ? c : a.tokens);
-    const int32_t steps = (int32_t)(((int64_t)c - b + kStepRows - 1) / kStepRows);
-    const int32_t each = (steps + a.pieces - 1) / a.pieces;
-    const int64_t lo = b + (int64_t)piece * each * kStepRows, hi = lo + (int64_t)each * kStepRows;
-    k0 = (int32_t)(lo < c ? lo : c);
-    k1 = (int32_t)(hi < c ? hi : c);
-}
-
 template <int W, bool BF16, bool F32, bool DIRECT>
 __global__ __launch_bounds__(Tile<W>::kLanes, Tile<W>::kWavesPerSimd) void expert_grad_kernel(ExpertArgs a) {
     __shared__ __align__(1024) char lds[Tile<W>::kLds];
@@ -159,8 +146,8 @@ __global__ __launch_bounds__(Tile<W>::kLanes, Tile<W>::kWavesPerSimd) void exper
     const int32_t e = (int32_t)(whole % (uint32_t)a.experts), piece = (int32_t)(whole / (uint32_t)a.experts);
     const int32_t ti = (int32_t)(group % per / gn * kBand + in / kBand), tj = (int32_t)(group % per % gn * kBand + in % kBand);
     if (ti >= a.mt || tj >= a.nt) return;
-    int32_t k0, k1;
-    expert_run(a, e, piece, k0, k1);
+    const Rows run = expert_piece(expert_run(a.offsets[e], a.offsets[e + 1], a.tokens), a.pieces, piece);
+    const int32_t k0 = run.first, k1 = run.end;
     if (k0 >= k1 && a.accumulate && !a.parts) return;
     const int32_t mleft = a.m - ti * Tile<W>::kSide, nleft = a.n - tj * Tile<W>::kSide;
     const char *x = a.x + k0 * a.ldx + (int64_t)ti * Tile<W>::kSide * 2, *y = a.dy + k0 * a.ldy + (int64_t)tj * Tile<W>::kSide * 2;
@@ -182,8 +169,7 @@ __global__ __launch_bounds__(Tile<W>::kLanes, Tile<W>::kWavesPerSimd) void exper
             char *next = lds + (half ^ 1) * Tile<W>::kStage;
             const uint32_t now = lds_at(lds) + half * Tile<W>::kStage;
             __syncthreads();
-            done += kStepRows;
-            const bool more = done < rows;
+            const bool more = next_step(done, rows);
             if (more) {
                 cx = load_chunks<W>(x + done * a.ldx, a.ldx, rows - done, mleft);
                 cy = load_chunks<W>(y + done * a.ldy, a.ldy, rows - done, nleft);
