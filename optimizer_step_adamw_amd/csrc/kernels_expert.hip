@@ -186,7 +186,7 @@ __global__ __launch_bounds__(Tile<W>::kLanes, Tile<W>::kWavesPerSimd) void exper
             write_chunks<W>(cy, next + Tile<W>::kOperand, nleft);
         }
     }
-    const float sc = a.scale ? *a.scale : 1.0f;
+    const float sc = rows > 0 && a.scale ? *a.scale : 1.0f;  // zeros whatever the scale
     // (a row's accesses before those of the row ahead of it: the compiler keeps
     // loads and stores of dW in order, and one at a time they would take a
     // memory latency each)
@@ -232,11 +232,18 @@ __global__ __launch_bounds__(Tile<W>::kLanes, Tile<W>::kWavesPerSimd) void exper
     }
 }
 
-// The pieces' sums in their order.
+// The pieces' sums in their order.  Experts without rows get zeros, or keep their
+// dW bit for bit, as they do in one piece.  (dW has at most 512 tiles here: its
+// elements count in 32 bits.)
 template <bool F32>
 __global__ __launch_bounds__(kThreads) void expert_join_kernel(ExpertArgs a) {
     const int64_t total = (int64_t)a.experts * a.m * a.n;
+    const uint32_t of = (uint32_t)a.m * (uint32_t)a.n;  // elements of an expert
     const float sc = a.scale ? *a.scale : 1.0f;
+    auto empty = [&](uint32_t x) {
+        const Rows run = expert_run(a.offsets[x], a.offsets[x + 1], a.tokens);
+        return run.first == run.end;
+    };
     for (int64_t e = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4; e < total; e += (int64_t)gridDim.x * kThreads * 4) {
         const int n = total - e < 4 ? (int)(total - e) : 4;
         f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -252,8 +259,22 @@ __global__ __launch_bounds__(kThreads) void expert_join_kernel(ExpertArgs a) {
         }
         x = x * sc;
         const bool vec = a.out_vec;
-        if (a.accumulate) x = dw_get<F32>(a.dw, e, n, vec) + x;
-        dw_put<F32>(a.dw, e, n, vec, x);
+        const uint32_t first = (uint32_t)e / of, last = (uint32_t)(e + n - 1) / of;
+        if (first == last && !empty(first)) {
+            if (a.accumulate) x = dw_get<F32>(a.dw, e, n, vec) + x;
+            dw_put<F32>(a.dw, e, n, vec, x);
+            continue;
+        }
+        // an expert without rows, or elements of several experts: one by one
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i >= n) break;
+            const bool none = empty((uint32_t)(e + i) / of);
+            if (none && a.accumulate) continue;
+            f32x4 y = {none ? 0.0f : x[i], 0.0f, 0.0f, 0.0f};
+            if (a.accumulate) y[0] = dw_get<F32>(a.dw, e + i, 1, false)[0] + y[0];
+            dw_put<F32>(a.dw, e + i, 1, false, y);
+        }
     }
 }
 
