@@ -14,13 +14,15 @@
  * Conventions for every entry point:
  *  - Returns OPTIM_OK (0) or a positive OPTIM_E* code; optim_last_error()
  *    then holds a message for the calling thread.  Nothing aborts, throws or
- *    blocks the host; a failed call has launched nothing.
+ *    blocks the host; a failed call has launched nothing.  A call for which
+ *    the host has too little memory fails with OPTIM_EINVAL.
  *  - "dev" pointers are device (HBM) pointers owned by the caller; "host"
  *    pointers are host memory owned by the caller.  The library allocates no
  *    device memory: plan metadata, per-step scalars and reduction partials
  *    live in a caller-owned workspace (or, for optim_plan_create_static, in
- *    the library's static device workspace).  The only host allocation is
- *    the plan object itself.
+ *    the library's static device workspace).  Host memory is
+ *    held by the plan object; plan creation and the checks of a call allocate
+ *    and free some while they run.
  *  - `stream` is a hipStream_t (NULL = the legacy default stream).  Every
  *    device-side effect is enqueued on it, in order; nothing reads device
  *    memory back to the host, so a whole step can be captured in a HIP graph.

@@ -12,8 +12,8 @@
 #include <atomic>
 #include <cmath>
 #include <cstring>
+#include <memory>
 #include <mutex>
-#include <new>
 #include <string>
 #include <vector>
 
@@ -44,6 +44,19 @@ int fail(int code, const std::string &msg) {
     g_err = msg;
     return code;
 }
+
+// What an entry point's body throws (the host is out of memory) becomes a status:
+// no exception leaves the library.
+int out_of_memory() noexcept {
+    try {
+        g_err = "the host is out of memory";
+    } catch (...) {
+        g_err = "no host memory";  // short enough to need none
+    }
+    return OPTIM_EINVAL;
+}
+#define OPTIM_CATCH \
+    catch (...) { return out_of_memory(); }
 
 #define HIP_OK(expr)                                                                 \
     do {                                                                             \
@@ -953,22 +966,22 @@ extern "C" {
 
 const char *optim_last_error(void) { return g_err.c_str(); }
 
-int optim_quant_codebook(int32_t bits, int32_t is_signed, float *values, float *thresholds) {
+int optim_quant_codebook(int32_t bits, int32_t is_signed, float *values, float *thresholds) try {
     if (bits != 8 && bits != 4) return fail(OPTIM_EINVAL, "bits must be 8 or 4");
     if (!values || !thresholds) return fail(OPTIM_EINVAL, "NULL output");
     dynamic_map(is_signed ? bits - 1 : bits, values, thresholds);
     return OPTIM_OK;
-}
+} OPTIM_CATCH
 
 int optim_plan_workspace_size(const optim_tensor_list *list, int32_t algo,
-                              const optim_plan_opts *opts, size_t *bytes) {
+                              const optim_plan_opts *opts, size_t *bytes) try {
     if (!bytes) return fail(OPTIM_EINVAL, "bytes is NULL");
     Built B;
     const int rc = build(list, algo, opts, B);
     if (rc) return rc;
     *bytes = B.L.total;
     return OPTIM_OK;
-}
+} OPTIM_CATCH
 
 }  // extern "C"
 
@@ -1068,13 +1081,15 @@ int create_on(const Built &B, const optim_tensor_list *list, int32_t algo, const
         if (!build_map(7, cb->m8) || !build_map(8, cb->v8) || !build_map(3, cb->m4) || !build_map(4, cb->v4))
             return fail(OPTIM_EUNSUPPORTED, "quantization map does not fit the bucket table");
     }
+    std::unique_ptr<optim_plan> owner(new optim_plan{});
+    optim_plan *P = owner.get();
+    P->segs = B.segs;
+    P->runs = B.runs;
     int cus = 0;
     HIP_OK(hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev));
     HIP_OK(hipMemcpyAsync(workspace, img.data(), img.size(), hipMemcpyHostToDevice, s));
     HIP_OK(hipStreamSynchronize(s));
 
-    optim_plan *P = new (std::nothrow) optim_plan{};
-    if (!P) return fail(OPTIM_EINVAL, "out of host memory");
     P->algo = algo;
     P->pk = list->param_dtype == OPTIM_F32 ? P_F32
             : !list->master                 ? P_BF16R
@@ -1094,8 +1109,6 @@ int create_on(const Built &B, const optim_tensor_list *list, int32_t algo, const
     P->state_dtype = opts ? opts->state_dtype : OPTIM_F32;
     P->ws = static_cast<char *>(workspace);
     P->L = B.L;
-    P->segs = B.segs;
-    P->runs = B.runs;
     P->lone0 = B.lone0;
     P->lone_narrow = B.lone_narrow;
     P->lone_unit0 = B.lone_unit0;
@@ -1108,7 +1121,7 @@ int create_on(const Built &B, const optim_tensor_list *list, int32_t algo, const
     P->ngitems = (int32_t)B.gitems.size();
     P->ngsmall = (int32_t)B.gsmall.size();
     P->gkeep0 = B.gkeep0;
-    *out = P;
+    *out = owner.release();
     return OPTIM_OK;
 }
 
@@ -1117,7 +1130,7 @@ int create_on(const Built &B, const optim_tensor_list *list, int32_t algo, const
 extern "C" {
 
 int optim_plan_create(const optim_tensor_list *list, int32_t algo, const optim_plan_opts *opts,
-                      void *workspace, size_t workspace_bytes, void *stream, optim_plan **out) {
+                      void *workspace, size_t workspace_bytes, void *stream, optim_plan **out) try {
     if (!out) return fail(OPTIM_EINVAL, "out is NULL");
     *out = nullptr;
     Built B;
@@ -1131,10 +1144,10 @@ int optim_plan_create(const optim_tensor_list *list, int32_t algo, const optim_p
     int dev = 0;
     HIP_OK(hipGetDevice(&dev));
     return create_on(B, list, algo, opts, workspace, static_cast<hipStream_t>(stream), dev, out);
-}
+} OPTIM_CATCH
 
 int optim_plan_create_static(const optim_tensor_list *list, int32_t algo, const optim_plan_opts *opts,
-                             void *stream, optim_plan **out) {
+                             void *stream, optim_plan **out) try {
     if (!out) return fail(OPTIM_EINVAL, "out is NULL");
     *out = nullptr;
     Built B;
@@ -1157,21 +1170,20 @@ int optim_plan_create_static(const optim_tensor_list *list, int32_t algo, const 
     P->static_gen = gen;
     *out = P;
     return OPTIM_OK;
-}
+} OPTIM_CATCH
 
-int optim_plan_destroy(optim_plan *plan) {
+int optim_plan_destroy(optim_plan *plan) try {
     if (plan) free_trace(plan);
     delete plan;
     return OPTIM_OK;
-}
+} OPTIM_CATCH
 
-int optim_plan_trace(optim_plan *plan, int32_t capacity) {
+int optim_plan_trace(optim_plan *plan, int32_t capacity) try {
     if (!plan) return fail(OPTIM_EINVAL, "plan is NULL");
     if (capacity < 0) return fail(OPTIM_EINVAL, "negative trace capacity");
     free_trace(plan);
     if (capacity == 0) return OPTIM_OK;
-    Trace *t = new (std::nothrow) Trace{};
-    if (!t) return fail(OPTIM_EINVAL, "out of host memory");
+    std::unique_ptr<Trace> t(new Trace{});
     t->recs.reserve((size_t)capacity);
     for (int32_t i = 0; i < capacity; ++i) {
         TraceRec r{nullptr, 0, nullptr, nullptr};
@@ -1181,18 +1193,18 @@ int optim_plan_trace(optim_plan *plan, int32_t capacity) {
             if (e != hipSuccess) (void)hipEventDestroy(r.start);
         }
         if (e != hipSuccess) {
-            plan->trace = t;
+            plan->trace = t.release();
             free_trace(plan);
             return fail(OPTIM_EHIP, std::string("hipEventCreate: ") + hipGetErrorString(e));
         }
         t->recs.push_back(r);
     }
-    plan->trace = t;
+    plan->trace = t.release();
     return OPTIM_OK;
-}
+} OPTIM_CATCH
 
 int optim_plan_trace_read(optim_plan *plan, optim_kernel_time *out, int32_t max, int32_t *count,
-                          int64_t *dropped) {
+                          int64_t *dropped) try {
     if (!plan || !count) return fail(OPTIM_EINVAL, "plan and count are required");
     if (max < 0 || (max > 0 && !out)) return fail(OPTIM_EINVAL, "need out[max], max >= 0");
     Trace *t = plan->trace;
@@ -1211,10 +1223,10 @@ int optim_plan_trace_read(optim_plan *plan, optim_kernel_time *out, int32_t max,
     *count = (int32_t)n;
     if (dropped) *dropped = lost;
     return OPTIM_OK;
-}
+} OPTIM_CATCH
 
 int optim_plan_set_schedule(optim_plan *plan, int32_t kind, double lr_max, double lr_min, int32_t K,
-                            int32_t *iter_dev) {
+                            int32_t *iter_dev) try {
     if (!plan) return fail(OPTIM_EINVAL, "plan is NULL");
     if (kind == OPTIM_SCHED_NONE) {
         plan->sched = OPTIM_SCHED_NONE;
@@ -1232,7 +1244,7 @@ int optim_plan_set_schedule(optim_plan *plan, int32_t kind, double lr_max, doubl
     plan->K = K;
     plan->iter_dev = iter_dev;
     return OPTIM_OK;
-}
+} OPTIM_CATCH
 
 }  // extern "C"
 
@@ -1412,7 +1424,7 @@ int check_adamw_hp(const optim_adamw_hp *hp) {
 extern "C" {
 
 int optim_step_adamw(optim_plan *plan, const optim_adamw_hp *hp, float *lr_dev, const float *inv_scale_dev,
-                     const float *found_inf_dev, int32_t *step_dev, void *stream) {
+                     const float *found_inf_dev, int32_t *step_dev, void *stream) try {
     int rc = check_plan(plan, OPTIM_ALGO_ADAMW, "optim_step_adamw");
     if (!rc) rc = check_adamw_hp(hp);
     if (rc) return rc;
@@ -1427,11 +1439,11 @@ int optim_step_adamw(optim_plan *plan, const optim_adamw_hp *hp, float *lr_dev, 
     else
         HIP_OK(launch_adamw(a, plan->pk, plan->gk, static_cast<hipStream_t>(stream)));
     return OPTIM_OK;
-}
+} OPTIM_CATCH
 
 int optim_step_ademamix(optim_plan *plan, const optim_ademamix_hp *hp, float *lr_dev,
                         const float *inv_scale_dev, const float *found_inf_dev, int32_t *step_dev,
-                        void *stream) {
+                        void *stream) try {
     int rc = check_plan(plan, OPTIM_ALGO_ADEMAMIX, "optim_step_ademamix");
     if (!rc) rc = check_ademamix_hp(hp);
     if (rc) return rc;
@@ -1442,10 +1454,10 @@ int optim_step_ademamix(optim_plan *plan, const optim_ademamix_hp *hp, float *lr
     const TraceScope ts(plan);
     HIP_OK(launch_ademamix(a, plan->pk, plan->gk, static_cast<hipStream_t>(stream)));
     return OPTIM_OK;
-}
+} OPTIM_CATCH
 
 int optim_step_adam_mini(optim_plan *plan, const optim_adamw_hp *hp, float *lr_dev, const float *inv_scale_dev,
-                         const float *found_inf_dev, int32_t *step_dev, void *stream) {
+                         const float *found_inf_dev, int32_t *step_dev, void *stream) try {
     int rc = check_plan(plan, OPTIM_ALGO_ADAM_MINI, "optim_step_adam_mini");
     if (!rc) rc = check_adamw_hp(hp);
     if (rc) return rc;
@@ -1457,10 +1469,10 @@ int optim_step_adam_mini(optim_plan *plan, const optim_adamw_hp *hp, float *lr_d
     HIP_OK(launch_adam_mini(a, plan->pk, plan->gk, plan->segs.data(), (int32_t)plan->segs.size(),
                             static_cast<hipStream_t>(stream)));
     return OPTIM_OK;
-}
+} OPTIM_CATCH
 
 int optim_step_lion(optim_plan *plan, const optim_lion_hp *hp, float *lr_dev, const float *inv_scale_dev,
-                    const float *found_inf_dev, int32_t *step_dev, void *stream) {
+                    const float *found_inf_dev, int32_t *step_dev, void *stream) try {
     int rc = check_plan(plan, OPTIM_ALGO_LION, "optim_step_lion");
     if (rc) return rc;
     if (!hp) return fail(OPTIM_EINVAL, "hyperparameters are NULL");
@@ -1471,10 +1483,10 @@ int optim_step_lion(optim_plan *plan, const optim_lion_hp *hp, float *lr_dev, co
     const TraceScope ts(plan);
     HIP_OK(launch_lion(a, plan->pk, plan->gk, static_cast<hipStream_t>(stream)));
     return OPTIM_OK;
-}
+} OPTIM_CATCH
 
 int optim_step_lamb(optim_plan *plan, const optim_adamw_hp *hp, float *lr_dev, const float *inv_scale_dev,
-                    const float *found_inf_dev, int32_t *step_dev, void *stream) {
+                    const float *found_inf_dev, int32_t *step_dev, void *stream) try {
     int rc = check_plan(plan, OPTIM_ALGO_LAMB, "optim_step_lamb");
     if (!rc) rc = check_adamw_hp(hp);
     if (rc) return rc;
@@ -1485,10 +1497,10 @@ int optim_step_lamb(optim_plan *plan, const optim_adamw_hp *hp, float *lr_dev, c
     const TraceScope ts(plan);
     HIP_OK(launch_lamb(a, plan->pk, plan->gk, static_cast<hipStream_t>(stream)));
     return OPTIM_OK;
-}
+} OPTIM_CATCH
 
 int optim_step_muon(optim_plan *plan, const optim_muon_hp *hp, float *lr_dev, const float *inv_scale_dev,
-                    const float *found_inf_dev, int32_t *step_dev, void *stream) {
+                    const float *found_inf_dev, int32_t *step_dev, void *stream) try {
     int rc = check_plan(plan, OPTIM_ALGO_MUON, "optim_step_muon");
     if (!rc) rc = check_muon_hp(hp);
     if (rc) return rc;
@@ -1512,11 +1524,11 @@ int optim_step_muon(optim_plan *plan, const optim_muon_hp *hp, float *lr_dev, co
     HIP_OK(launch_muon(a, ma, plan->pk, plan->gk, hp->steps, hp->nesterov != 0, plan->runs.data(),
                        (int32_t)plan->runs.size(), static_cast<hipStream_t>(stream)));
     return OPTIM_OK;
-}
+} OPTIM_CATCH
 
 int optim_step_8bit_blockwise(optim_plan *plan, const optim_adamw_hp *hp, int32_t bits, int32_t block,
                               float *lr_dev, const float *inv_scale_dev, const float *found_inf_dev,
-                              int32_t *step_dev, void *stream) {
+                              int32_t *step_dev, void *stream) try {
     int rc = check_plan(plan, OPTIM_ALGO_BLOCKWISE, "optim_step_8bit_blockwise");
     if (!rc) rc = check_adamw_hp(hp);
     if (rc) return rc;
@@ -1529,11 +1541,11 @@ int optim_step_8bit_blockwise(optim_plan *plan, const optim_adamw_hp *hp, int32_
     const TraceScope ts(plan);
     HIP_OK(launch_blockwise(a, plan->gk, false, static_cast<hipStream_t>(stream)));
     return OPTIM_OK;
-}
+} OPTIM_CATCH
 
 int optim_step_8bit_blockwise_ademamix(optim_plan *plan, const optim_ademamix_hp *hp, int32_t bits, int32_t block,
                                        float *lr_dev, const float *inv_scale_dev, const float *found_inf_dev,
-                                       int32_t *step_dev, void *stream) {
+                                       int32_t *step_dev, void *stream) try {
     int rc = check_plan(plan, OPTIM_ALGO_BLOCKWISE_ADEMAMIX, "optim_step_8bit_blockwise_ademamix");
     if (!rc) rc = check_ademamix_hp(hp);
     if (rc) return rc;
@@ -1546,9 +1558,9 @@ int optim_step_8bit_blockwise_ademamix(optim_plan *plan, const optim_ademamix_hp
     const TraceScope ts(plan);
     HIP_OK(launch_blockwise(a, plan->gk, true, static_cast<hipStream_t>(stream)));
     return OPTIM_OK;
-}
+} OPTIM_CATCH
 
-int optim_check_finite(optim_plan *plan, float *found_inf_dev, void *stream) {
+int optim_check_finite(optim_plan *plan, float *found_inf_dev, void *stream) try {
     if (!plan) return fail(OPTIM_EINVAL, "plan is NULL");
     if (int rc = check_live(plan, "optim_check_finite")) return rc;
     if (plan->algo == OPTIM_ALGO_GRADS)
@@ -1562,10 +1574,10 @@ int optim_check_finite(optim_plan *plan, float *found_inf_dev, void *stream) {
     const TraceScope ts(plan);
     HIP_OK(launch_check_finite(a, plan->gk, static_cast<hipStream_t>(stream)));
     return OPTIM_OK;
-}
+} OPTIM_CATCH
 
 int optim_grad_norm(optim_plan *plan, const float *inv_scale_dev, double max_norm, float *found_inf_dev,
-                    float *norm_dev, float *clip_inv_scale_dev, void *stream) {
+                    float *norm_dev, float *clip_inv_scale_dev, void *stream) try {
     if (!plan) return fail(OPTIM_EINVAL, "plan is NULL");
     if (int rc = check_live(plan, "optim_grad_norm")) return rc;
     if (plan->algo == OPTIM_ALGO_GRADS)
@@ -1583,10 +1595,10 @@ int optim_grad_norm(optim_plan *plan, const float *inv_scale_dev, double max_nor
     HIP_OK(launch_grad_norm(a, plan->gk, inv_scale_dev, max_norm, norm_dev, clip_inv_scale_dev,
                             static_cast<hipStream_t>(stream)));
     return OPTIM_OK;
-}
+} OPTIM_CATCH
 
 int optim_grad_norms(optim_plan *plan, int32_t kind, const float *inv_scale_dev, double max_norm,
-                     float *found_inf_dev, float *norms_dev, float *total_dev, float *coef_dev, void *stream) {
+                     float *found_inf_dev, float *norms_dev, float *total_dev, float *coef_dev, void *stream) try {
     if (const int rc = check_plan(plan, OPTIM_ALGO_GRADS, "optim_grad_norms")) return rc;
     if (const int rc = check_norm_args(kind, inv_scale_dev, max_norm, total_dev, coef_dev)) return rc;
     if (!total_dev) return fail(OPTIM_EINVAL, "total_dev must be an aligned device float");
@@ -1595,10 +1607,10 @@ int optim_grad_norms(optim_plan *plan, int32_t kind, const float *inv_scale_dev,
     HIP_OK(launch_grad_norms(grad_args(plan), plan->gk, kind, inv_scale_dev, max_norm, found_inf_dev, norms_dev,
                              total_dev, coef_dev, static_cast<hipStream_t>(stream)));
     return OPTIM_OK;
-}
+} OPTIM_CATCH
 
 int optim_clip_coef(const float *norms_dev, int64_t count, int32_t kind, const float *inv_scale_dev, double max_norm,
-                    float *total_dev, float *coef_dev, void *stream) {
+                    float *total_dev, float *coef_dev, void *stream) try {
     if (count < 0) return fail(OPTIM_EINVAL, "negative count");
     if (count > 0 && !norms_dev) return fail(OPTIM_EINVAL, "NULL norms");
     if (!aligned(norms_dev, 4)) return fail(OPTIM_EALIGN, "norms misaligned");
@@ -1606,29 +1618,29 @@ int optim_clip_coef(const float *norms_dev, int64_t count, int32_t kind, const f
     HIP_OK(launch_clip_coef(norms_dev, count, kind, inv_scale_dev, max_norm, total_dev, coef_dev,
                             static_cast<hipStream_t>(stream)));
     return OPTIM_OK;
-}
+} OPTIM_CATCH
 
-int optim_clip_grads(optim_plan *plan, const float *coef_dev, const float *found_inf_dev, void *stream) {
+int optim_clip_grads(optim_plan *plan, const float *coef_dev, const float *found_inf_dev, void *stream) try {
     if (const int rc = check_plan(plan, OPTIM_ALGO_GRADS, "optim_clip_grads")) return rc;
     if (!coef_dev || !aligned(coef_dev, 4)) return fail(OPTIM_EINVAL, "coef_dev must be an aligned device float");
     if (!aligned(found_inf_dev, 4)) return fail(OPTIM_EALIGN, "scalar pointer misaligned");
     const TraceScope ts(plan);
     HIP_OK(launch_clip_grads(grad_args(plan), plan->gk, coef_dev, found_inf_dev, static_cast<hipStream_t>(stream)));
     return OPTIM_OK;
-}
+} OPTIM_CATCH
 
-int optim_expert_grad_workspace(int32_t experts, int64_t tokens, int64_t m, int64_t n, size_t *bytes) {
+int optim_expert_grad_workspace(int32_t experts, int64_t tokens, int64_t m, int64_t n, size_t *bytes) try {
     if (!bytes) return fail(OPTIM_EINVAL, "bytes is NULL");
     if (const int rc = check_expert_sizes(experts, tokens, m, n)) return rc;
     const int32_t pieces = expert_pieces(experts, tokens, m, n);
     *bytes = pieces > 1 ? (size_t)pieces * experts * m * n * sizeof(float) : 0;
     return OPTIM_OK;
-}
+} OPTIM_CATCH
 
 int optim_expert_grad(const void *x_dev, int64_t ldx, const void *dy_dev, int64_t ldy, int32_t in_dtype,
                       const int32_t *offsets_dev, int32_t experts, int64_t tokens, int64_t m, int64_t n, void *dw_dev,
                       int32_t dw_dtype, int32_t accumulate, const float *scale_dev, void *workspace,
-                      size_t workspace_bytes, void *stream) {
+                      size_t workspace_bytes, void *stream) try {
     if (const int rc = check_expert_sizes(experts, tokens, m, n)) return rc;
     if (in_dtype != OPTIM_BF16 && in_dtype != OPTIM_F16)
         return fail(OPTIM_EDTYPE, "in_dtype must be OPTIM_BF16 or OPTIM_F16");
@@ -1683,11 +1695,11 @@ int optim_expert_grad(const void *x_dev, int64_t ldx, const void *dy_dev, int64_
     HIP_OK(launch_expert_grad(a, in_dtype == OPTIM_BF16, dw_dtype == OPTIM_F32, direct,
                               static_cast<hipStream_t>(stream)));
     return OPTIM_OK;
-}
+} OPTIM_CATCH
 
 int optim_scaler_update(float *scale_dev, float *inv_scale_dev, int32_t *growth_tracker_dev,
                         const float *found_inf_dev, double growth_factor, double backoff_factor,
-                        int32_t growth_interval, void *stream) {
+                        int32_t growth_interval, void *stream) try {
     if (!scale_dev || !growth_tracker_dev || !found_inf_dev)
         return fail(OPTIM_EINVAL, "scale, growth tracker and found_inf are required");
     if (!aligned(scale_dev, 4) || !aligned(inv_scale_dev, 4) || !aligned(growth_tracker_dev, 4) ||
@@ -1700,10 +1712,10 @@ int optim_scaler_update(float *scale_dev, float *inv_scale_dev, int32_t *growth_
     HIP_OK(launch_scaler_update(scale_dev, inv_scale_dev, growth_tracker_dev, found_inf_dev, growth_factor,
                                 backoff_factor, growth_interval, static_cast<hipStream_t>(stream)));
     return OPTIM_OK;
-}
+} OPTIM_CATCH
 
 int optim_quantize_blockwise(optim_plan *plan, int32_t is_signed, const float *x_dev, int64_t n,
-                             uint8_t *codes_dev, float *absmax_dev, void *stream) {
+                             uint8_t *codes_dev, float *absmax_dev, void *stream) try {
     int rc = check_blockwise_plan(plan, "optim_quantize_blockwise");
     if (rc) return rc;
     if (n < 0) return fail(OPTIM_EINVAL, "negative n");
@@ -1714,10 +1726,10 @@ int optim_quantize_blockwise(optim_plan *plan, int32_t is_signed, const float *x
                            plan->block, is_signed ? 1 : 0, x_dev, n, codes_dev, absmax_dev,
                            static_cast<hipStream_t>(stream)));
     return OPTIM_OK;
-}
+} OPTIM_CATCH
 
 int optim_dequantize_blockwise(optim_plan *plan, int32_t is_signed, const uint8_t *codes_dev,
-                               const float *absmax_dev, int64_t n, float *x_dev, void *stream) {
+                               const float *absmax_dev, int64_t n, float *x_dev, void *stream) try {
     int rc = check_blockwise_plan(plan, "optim_dequantize_blockwise");
     if (rc) return rc;
     if (n < 0) return fail(OPTIM_EINVAL, "negative n");
@@ -1728,10 +1740,10 @@ int optim_dequantize_blockwise(optim_plan *plan, int32_t is_signed, const uint8_
                              plan->block, is_signed ? 1 : 0, codes_dev, absmax_dev, n, x_dev,
                              static_cast<hipStream_t>(stream)));
     return OPTIM_OK;
-}
+} OPTIM_CATCH
 
 int optim_remainder_split(const float *master_dev, uint16_t *bf16_dev, int16_t *rem_dev, int64_t n,
-                          void *stream) {
+                          void *stream) try {
     if (n < 0) return fail(OPTIM_EINVAL, "negative n");
     if (n == 0) return OPTIM_OK;
     if (!master_dev || !bf16_dev || !rem_dev) return fail(OPTIM_EINVAL, "NULL buffer");
@@ -1739,10 +1751,10 @@ int optim_remainder_split(const float *master_dev, uint16_t *bf16_dev, int16_t *
         return fail(OPTIM_EALIGN, "buffer misaligned");
     HIP_OK(launch_remainder_split(master_dev, bf16_dev, rem_dev, n, static_cast<hipStream_t>(stream)));
     return OPTIM_OK;
-}
+} OPTIM_CATCH
 
 int optim_remainder_reconstruct(const uint16_t *bf16_dev, const int16_t *rem_dev, float *master_dev, int64_t n,
-                                void *stream) {
+                                void *stream) try {
     if (n < 0) return fail(OPTIM_EINVAL, "negative n");
     if (n == 0) return OPTIM_OK;
     if (!master_dev || !bf16_dev || !rem_dev) return fail(OPTIM_EINVAL, "NULL buffer");
@@ -1750,6 +1762,6 @@ int optim_remainder_reconstruct(const uint16_t *bf16_dev, const int16_t *rem_dev
         return fail(OPTIM_EALIGN, "buffer misaligned");
     HIP_OK(launch_remainder_reconstruct(bf16_dev, rem_dev, master_dev, n, static_cast<hipStream_t>(stream)));
     return OPTIM_OK;
-}
+} OPTIM_CATCH
 
 }  // extern "C"
