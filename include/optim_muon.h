@@ -58,9 +58,17 @@ typedef struct optim_muon_hp {
  *                 X <- a X + B X
  *   p <- p - (lr wd p + lr f X),  f the factor above
  * m in fp32 without contraction; the sum of squares in fp64.  X, A and B are
- * kept as sums of two fp16 numbers (22 significant bits) and multiplied on
- * the matrix cores as three products of parts with fp32 sums, so the update
- * agrees with the same iteration in fp32 to about 1e-6 of its size.
+ * kept as sums of two fp16 numbers and multiplied on the matrix cores as three
+ * products of parts with fp32 sums (the product of both low parts, 2^-22 of the
+ * whole, is left out).  An element has 22 significant bits down to 2^-15 (of
+ * X, whose norm is 1 at first), below that an absolute error of up to 2^-37,
+ * which the iteration raises as it raises small singular values (a each step,
+ * 485 for five).  So the update agrees with the exact one as an fp32
+ * iteration's does, to 1e-6 (64 x 64) to 3e-6 (4096 x 4096) of its norm,
+ * where no part of the matrix is far smaller than the rest; beside elements
+ * 1e6 to 1e9 times as large to 4e-6 to 1.3e-5 of its norm, where fp32 comes to
+ * 1e-7; and rows 1e-6 of the others' size are updated to 2e-4 (64 x 64) to
+ * 1.3e-2 (4096 x 4096) of their own small update.
  * Orders of summation are fixed: results repeat bit for bit.
  * A matrix of zeros (an expert without tokens, fresh momentum) has update 0.
  * The polynomial must keep X within what the 16-bit parts hold: the bounds

@@ -12,7 +12,10 @@ namespace {
 // X, A and B are stored times 2^12: bounded by 15 (checked on the host) they
 // stay below fp16's 65504, and a typical element of a 4096 x 4096 X, 2^-12 at
 // the start and 2^-6 at the end, has both its parts well above fp16's
-// smallest subnormal, 2^-24.
+// smallest subnormal, 2^-24.  An element below 2^-15 may have a subnormal low
+// part and is then off by up to 2^-37: rows 1e-6 of the others' size get their
+// update to 2e-4 (64 x 64) to 1.3e-2 (4096 x 4096) of it only.  (Low parts with
+// a scale of their own would keep 22 bits there, but need sums of their own.)
 constexpr float kMuonScale = 4096.0f, kMuonUnscale = 1.0f / 4096.0f;
 
 __device__ __forceinline__ bool skipped(const StepArgs &a) {
