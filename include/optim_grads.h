@@ -85,17 +85,19 @@ int optim_clip_grads(optim_plan *plan, const float *coef_dev,
  * micro-batches of a step into fp32 loses nothing to 16 bits in between.
  * An expert without rows gets zeros (or keeps dW_e).  offsets_dev (device
  * int32[experts + 1]) is read by the kernel, so routing needs no host
- * synchronisation; each bound is clamped to [0, tokens] and to the one before
- * it.  Rows outside every run are not read.
+ * synchronisation; each bound is clamped to [0, tokens], and a run's end to
+ * its own beginning.  (Bounds are meant to ascend: where one is below the one
+ * before it, that run is empty and the next begins there, so rows may count
+ * for two experts.)  Rows outside every run are not read.
  * Runs are summed in one piece, or, where the tiles of dW are too few to fill
  * the GPU, in pieces through `workspace` (device, 256-byte aligned,
  * optim_expert_grad_workspace bytes, contents free between calls); NULL
  * sums in one piece, too few bytes are OPTIM_EWORKSPACE.  Either way the order of
  * sums is fixed by the sizes: results repeat bit for bit.
  * tokens < 2^31; m, n < 2^24; fewer than 2^18 blocks of 512 x 512 over all
- * experts (an expert is at least one); ldx >= m, ldy >= n.  dW must not
- * overlap X, dY or the workspace.  16-byte aligned X and dY with m, n, ldx
- * and ldy multiples of 8 take the fastest path.                            */
+ * experts (an expert is at least one); m <= ldx < 2^24, n <= ldy < 2^24.  dW
+ * must not overlap X, dY, offsets_dev or the workspace.  16-byte aligned X and
+ * dY with m, n, ldx and ldy multiples of 8 take the fastest path.          */
 int optim_expert_grad_workspace(int32_t experts, int64_t tokens, int64_t m,
                                 int64_t n, size_t *bytes);
 int optim_expert_grad(const void *x_dev, int64_t ldx, const void *dy_dev,
