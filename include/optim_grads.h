@@ -42,10 +42,13 @@ enum { OPTIM_NORM_L2 = 0, OPTIM_NORM_L1 = 1, OPTIM_NORM_INF = 2 };
  * found_inf_dev (may be NULL) is set to 1.0f if any element is NaN or +-Inf
  * and left unchanged otherwise, as by optim_check_finite; the norms of the
  * tensors concerned and the total are then not finite, and coef = s.
- * Sums are kept in fp64 in an order fixed by the list, so results repeat bit
- * for bit; a finite list has finite norms (up to fp32's range), and
- * gradients whose squares leave fp32's range at either end are summed
- * exactly.                                                                 */
+ * A 16-byte group of 4 or 8 elements is summed in fp32 and the groups in
+ * fp64, so a sum is within 7 * 2^-24 of itself.  Where an item (a run of a
+ * tensor's elements, or a small tensor) has a largest magnitude from which
+ * fp32 sums could overflow (2^62 for L2, 2^120 for L1) or below 2^-40, its
+ * elements are summed again in fp64 alone.  The order of sums is fixed by the
+ * list and by where its arrays begin within 16 bytes, so results repeat bit
+ * for bit; a finite list has finite norms (up to fp32's range).           */
 int optim_grad_norms(optim_plan *plan, int32_t kind, const float *inv_scale_dev,
                      double max_norm, float *found_inf_dev, float *norms_dev,
                      float *total_dev, float *coef_dev, void *stream);

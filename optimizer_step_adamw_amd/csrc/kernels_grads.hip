@@ -70,11 +70,13 @@ __device__ __forceinline__ void grad_store1(char *p, int64_t e, uint32_t b) {
 }
 
 // ---------------------------------------------------------------- norms
-// A lane's part: the sum in fp64 over fp32 sums of one 16-byte group each
-// (4 or 8 elements: at most 3 fp32 additions, so the rounding of a group is
-// 2^-22 and averages out; a square in fp64 on every element measured 13%
-// slower on a 1.1B bf16 list), and the largest magnitude as fp32 bits, which
-// also tells whether the fp32 part was in range and whether all is finite.
+// A lane's part: the sum in fp64 over fp32 sums of one 16-byte group each, and
+// the largest magnitude as fp32 bits, which also tells whether the fp32 part was
+// in range and whether all is finite.  A group is a chain of 4 (fp32) or 8
+// elements: at most 4 roundings for fp32 squares, the first that of a square;
+// 7 for 16-bit ones and for magnitudes, whose first is exact: 7 * 2^-24 of the
+// group at most, half of that of a norm of squares, and less on average.  (A
+// square in fp64 on every element measured 13% slower on a 1.1B bf16 list.)
 struct NormAcc {
     double s = 0.0;
     uint32_t mx = 0;
