@@ -2,8 +2,8 @@
 // (optim_expert_grad): dW_e (+)= s X_e^T dY_e, one product per expert over
 // its own run of rows.
 //
-// A workgroup computes a 128 x 128 tile of one expert's dW with the product of
-// tiles.h, both operands' k (the rows) running down memory.  Whole steps of 64
+// A workgroup computes a 128 x 128 tile of one expert's dW, or a 256 x 256 one,
+// with the product of tiles.h, both operands' k (the rows) running down memory.  Whole steps of 64
 // rows go straight from global memory into LDS; the rows left over, and every
 // step where a row is not a whole number of aligned 16-byte chunks, pass
 // through registers, where what lies outside the run or the matrix becomes
@@ -11,10 +11,10 @@
 //
 // Bound by the matrix cores where runs are long, by writing dW where they are
 // short.  Measured on MI355X: 8 experts 2048 x 8192 over 16384 rows,
-// accumulated in fp32, 616 us (550 GFLOP, 893 TFLOP/s, and 1.4 GB of rows and
-// gradients; the matrix cores busy 42%), 64 experts 2048 x 1024 over 65536 rows
-// in bf16 367 us (275 GFLOP, 749 TFLOP/s, 0.67 GB), 4 experts 256 x 172 over
-// 512 rows 11.8 us.
+// accumulated in fp32, 616-624 us (550 GFLOP, 881-893 TFLOP/s, and 1.4 GB of
+// rows and gradients; the matrix cores busy 42%; up to 760 in the first 15 calls
+// after a pause), 64 experts 2048 x 1024 over 65536 rows in bf16 367-373 us (275
+// GFLOP, 737-749 TFLOP/s, 0.67 GB), 4 experts 256 x 172 over 300 rows 11.8 us.
 #include "optim_grads.h"
 
 #include "expert_rows.h"
@@ -338,8 +338,13 @@ int32_t expert_pieces(int32_t experts, int64_t tokens, int64_t m, int64_t n) {
 // Wide tiles where they fill the GPU (one workgroup a compute unit): measured
 // on MI355X, 8 experts 2048x8192 over 16384 rows, accumulated in fp32, 616 us
 // against 733 with narrow ones, 64 experts 2048x1024 over 65536 rows in bf16
-// 310 (runs of equal length) against 388; 8 experts 512x2048 over 8192 rows, 128 wide tiles, 44
-// against 31.  Only whole 16-byte chunks go that way.
+// 310 (runs of equal length) against 388; 8 experts 512x2048 over 8192 rows, 128
+// wide tiles, 44 against 31.  Only whole 16-byte chunks go that way.  The rule
+// counts tiles, not how much of them is dW or how many steps a run has, and loses
+// where sides are just past a tile or runs short: over 65536 rows, wide and
+// narrow, 256 experts 128x128 60 and 23 us, 64 of 64x1040 57 and 41, of 264x264 58
+// and 37, of 512x512 64 and 48, 128 of 384x384 81 and 42; 64 of 640x640 103 and
+// 153.
 hipError_t launch_expert_grad(const ExpertArgs &a, bool bf16, bool out_f32, bool direct, hipStream_t s) {
     const int64_t wide = (int64_t)a.experts * tiles_of<2>(a.m) * tiles_of<2>(a.n);
     return direct && wide >= 256 ? launch_expert_w<2>(a, bf16, out_f32, direct, s)

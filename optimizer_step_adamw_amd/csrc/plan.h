@@ -228,7 +228,10 @@ constexpr int64_t kMuonUnit = 4096;  // elements of padded X per workgroup of th
 constexpr int32_t kMuonSlab = 16384;
 constexpr int64_t kMuonMaxSlabs = 512, kMuonSlabRoom = 768;
 // Shorter side of matrices that may take wide tiles (from 400 on, 48 matrices
-// of 1000 x 408 took 1267 us instead of 1131).
+// of 1000 x 408 took 1267 us instead of 1131).  Right from 768 on, where wide
+// tiles gain (64 matrices of 768 x 768 2717 us, 2816 by narrow ones; 4 of 2048 x
+// 2048 2373 and 2478); between, a side fills too little of its last tile (64 of 512
+// x 512 1145 and 1055, of 520 x 600 1989 and 1502, of 640 x 640 2292 and 1837).
 constexpr int64_t kMuonWideMin = 512;
 // Tiles of A and of A A are summed in pieces where few workgroups would have
 // long sums: a piece is of the steps (of 32) that would share all tiles' steps
@@ -236,7 +239,9 @@ constexpr int64_t kMuonWideMin = 512;
 // is kMuonPieceGain steps longer.  The pieces are joined by a launch of their
 // own.  Measured, A whole and in pieces with the joining: 640 x 640 22.8 and
 // 17.7 us (20 steps, 2 pieces), 1024 x 1024 27.5 and 18.2, 3981 x 136 66.4 and
-// 22.1.
+// 22.1.  Runs of wide tiles sum whole, also where a short side leaves A few tiles:
+// a step of one 512 x 65536 takes 6193 us so, by narrow tiles and pieces 1464; of
+// one 1024 x 50304 6513 and 3002.
 constexpr int64_t kMuonPieceMin = 8, kMuonPieceGain = 12;
 constexpr int64_t kMuonMaxSide = int64_t(1) << 20;
 constexpr int64_t kMuonRunBytes = int64_t(4) << 30;  // workspace of one run of launches
@@ -281,8 +286,8 @@ struct MuonRun {          // matrices [mat0, mat1) that share a run of launches
 struct Layout {
     size_t counters, group_wd, tensors, spans, codebook, partials, blockfac,
         blockspan, packs, pack_off, pack_td, total;
-    // gradient lists: tensors, items, the bundled tensors' indexes, arrival
-    // counters and sums of the tensors
+    // gradient lists: items, small tensors, arrival counters and sums of the
+    // tensors
     size_t gitems, gsmall, gcount, gsum;
     // Muon: matrices, tiles of the symmetric products and of X, the region
     // the runs share
