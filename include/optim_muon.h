@@ -33,7 +33,8 @@ extern "C" {
  * The workspace holds, for every matrix of the largest run, about 8 bytes an
  * element and 8 bytes times the square of its shorter side, sides rounded up
  * to 32 (with a side of at most 128: up to 12 bytes an element, that side
- * rounded up to 64 or 128), and up to 64 MB beside.
+ * rounded up to 64 or 128), up to 64 MB beside, and tables of about 150 bytes
+ * a matrix of the plan.
  * optim_check_finite, optim_grad_norm, optim_plan_set_schedule and
  * optim_plan_trace take such a plan as any other.                          */
 
