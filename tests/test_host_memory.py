@@ -34,7 +34,8 @@ few, many = {"muon": (muon(10), muon(1 << 22)), "grads": (grads(10), grads(1 << 
 assert few() > 0
 pages = int(open("/proc/self/statm").read().split()[0])
 bound = pages * resource.getpagesize() + (48 << 20)  # 48 MiB more than now
-resource.setrlimit(resource.RLIMIT_AS, (bound, resource.RLIM_INFINITY))
+before = resource.getrlimit(resource.RLIMIT_AS)
+resource.setrlimit(resource.RLIMIT_AS, (bound, before[1]))
 try:
     many()
 except osa.OptimError as e:
@@ -42,7 +43,7 @@ except osa.OptimError as e:
 else:
     raise SystemExit("not refused")
 assert few() > 0  # the library goes on
-resource.setrlimit(resource.RLIMIT_AS, (resource.RLIM_INFINITY, resource.RLIM_INFINITY))
+resource.setrlimit(resource.RLIMIT_AS, before)
 assert many() > 0
 print("fine")
 """
