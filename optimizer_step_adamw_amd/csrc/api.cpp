@@ -6,6 +6,7 @@
 #include "optim_grads.h"
 #include "optim_muon.h"
 #include "optim_step.h"
+#include "api_common.h"
 #include "plan.h"
 
 #include <algorithm>
@@ -36,17 +37,16 @@ TraceRec *trace_slot(const char *name, int64_t grid) {
 }
 }  // namespace optim
 
+namespace optim {
 namespace {
-
 thread_local std::string g_err;
+}
 
 int fail(int code, const std::string &msg) {
     g_err = msg;
     return code;
 }
 
-// What an entry point's body throws (the host is out of memory) becomes a status:
-// no exception leaves the library.
 int out_of_memory() noexcept {
     try {
         g_err = "the host is out of memory";
@@ -55,19 +55,29 @@ int out_of_memory() noexcept {
     }
     return OPTIM_EINVAL;
 }
-#define OPTIM_CATCH \
-    catch (...) { return out_of_memory(); }
 
-#define HIP_OK(expr)                                                                 \
-    do {                                                                             \
-        hipError_t e_ = (expr);                                                      \
-        if (e_ != hipSuccess)                                                        \
-            return fail(OPTIM_EHIP, std::string(#expr) + ": " + hipGetErrorString(e_)); \
-    } while (0)
+int check_overlaps(std::vector<Range> &ranges) {
+    std::sort(ranges.begin(), ranges.end(), [](const Range &a, const Range &b) { return a.lo < b.lo; });
+    uintptr_t end_all = 0, end_w = 0;
+    const Range *cov_all = nullptr, *cov_w = nullptr;
+    for (const Range &r : ranges) {
+        const Range *hit = nullptr;
+        if (r.written && r.lo < end_all) hit = cov_all;
+        else if (!r.written && r.lo < end_w) hit = cov_w;
+        if (hit)
+            return fail(OPTIM_EINVAL, "buffers overlap: tensor " + std::to_string(hit->tensor) + " " +
+                                          hit->what + " and tensor " + std::to_string(r.tensor) + " " +
+                                          r.what);
+        if (r.hi > end_all) { end_all = r.hi; cov_all = &r; }
+        if (r.written && r.hi > end_w) { end_w = r.hi; cov_w = &r; }
+    }
+    return OPTIM_OK;
+}
+}  // namespace optim
+
+namespace {
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // ---------------------------------------------------------------- codebook
 // Dynamic map with mb magnitude bits (see optim_quant_codebook).
@@ -154,32 +164,6 @@ struct Built {
     int64_t lone_unit0 = 0;
     Layout L{};
 };
-
-struct Range {
-    uintptr_t lo, hi;
-    bool written;
-    int tensor;
-    const char *what;
-};
-
-// no written buffer may overlap any other buffer of the plan
-int check_overlaps(std::vector<Range> &ranges) {
-    std::sort(ranges.begin(), ranges.end(), [](const Range &a, const Range &b) { return a.lo < b.lo; });
-    uintptr_t end_all = 0, end_w = 0;
-    const Range *cov_all = nullptr, *cov_w = nullptr;
-    for (const Range &r : ranges) {
-        const Range *hit = nullptr;
-        if (r.written && r.lo < end_all) hit = cov_all;
-        else if (!r.written && r.lo < end_w) hit = cov_w;
-        if (hit)
-            return fail(OPTIM_EINVAL, "buffers overlap: tensor " + std::to_string(hit->tensor) + " " +
-                                          hit->what + " and tensor " + std::to_string(r.tensor) + " " +
-                                          r.what);
-        if (r.hi > end_all) { end_all = r.hi; cov_all = &r; }
-        if (r.written && r.hi > end_w) { end_w = r.hi; cov_w = &r; }
-    }
-    return OPTIM_OK;
-}
 
 int check_hp_beta(double b, const char *name) {
     if (!(b >= 0.0 && b < 1.0))
