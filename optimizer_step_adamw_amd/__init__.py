@@ -4,8 +4,8 @@ for AMD Instinct MI355X (gfx950).
 Argument marshalling only: torch tensors are turned into device pointers and a
 HIP stream handle; every step of the computation runs in the library's HIP
 kernels.  Functions keep the C names of ``include/optim_step.h``,
-``include/optim_grads.h`` and ``include/optim_muon.h``.  If the
-library has not been built, importing the binding works but every call raises
+``include/optim_grads.h``, ``include/optim_muon.h``, ``include/optim_route.h``
+and ``include/optim_dropout.h``.  If the library has not been built, importing the binding works but every call raises
 ``RuntimeError`` -- there is no fallback path.
 """
 from __future__ import annotations
@@ -26,6 +26,7 @@ OPTIM_NORM_L2, OPTIM_NORM_L1, OPTIM_NORM_INF = range(3)
 OPTIM_MUON_SCALE_NONE, OPTIM_MUON_SCALE_ASPECT, OPTIM_MUON_SCALE_RMS = range(3)
 OPTIM_MINI_FULL_V, OPTIM_MINI_HEAD, OPTIM_MINI_SCALAR = range(3)
 OPTIM_SCHED_NONE, OPTIM_SCHED_COSINE = 0, 1
+OPTIM_ROUTE_SOFTMAX, OPTIM_ROUTE_SIGMOID = 0, 1
 
 EXPORTED = (
     "optim_last_error", "optim_plan_workspace_size", "optim_plan_create", "optim_plan_destroy",
@@ -41,6 +42,11 @@ EXPORTED_GRADS = ("optim_grad_norms", "optim_clip_coef", "optim_clip_grads", "op
                   "optim_expert_grad")
 # entry points of include/optim_muon.h
 EXPORTED_MUON = ("optim_step_muon",)
+# entry points of include/optim_route.h
+EXPORTED_ROUTE = ("optim_route", "optim_route_grad", "optim_step_route_bias", "optim_route_rows_workspace",
+                  "optim_route_rows", "optim_expert_gather", "optim_expert_combine", "optim_expert_combine_grad")
+# entry points of include/optim_dropout.h
+EXPORTED_DROPOUT = ("optim_dropout",)
 # bytes of the library's static per-device workspace (optim_plan_create_static)
 OPTIM_STATIC_WORKSPACE_BYTES = 16 << 20
 
@@ -105,6 +111,23 @@ class optim_muon_hp(ctypes.Structure):
         super().__init__(momentum, eps, a, b, c, steps, nesterov, scale_kind)
 
 
+class optim_route_hp(ctypes.Structure):
+    """Softmax over all experts, the chosen weights summing to one, by default."""
+    _fields_ = [("topk", ctypes.c_int32), ("score", ctypes.c_int32), ("renormalise", ctypes.c_int32),
+                ("groups", ctypes.c_int32), ("top_groups", ctypes.c_int32), ("group_best", ctypes.c_int32),
+                ("scale", ctypes.c_double)]
+
+    def __init__(self, topk, score=OPTIM_ROUTE_SOFTMAX, renormalise=1, groups=1, top_groups=1, group_best=1, scale=1.0):
+        super().__init__(topk, score, renormalise, groups, top_groups, group_best, scale)
+
+
+class optim_dropout_hp(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_uint64), ("first", ctypes.c_int64), ("site", ctypes.c_uint32)]
+
+    def __init__(self, p, seed, site=0, first=0):
+        super().__init__(p, seed, first, site)
+
+
 _lib = None
 
 
@@ -152,6 +175,17 @@ def lib() -> ctypes.CDLL:
             "optim_clip_coef": ([_P, i64, i32, _P, f64, _P, _P, _P], i32),
             "optim_clip_grads": ([_P, _P, _P, _P], i32),
             "optim_expert_grad_workspace": ([i32, i64, i64, i64, ctypes.POINTER(sz)], i32),
+            "optim_route": ([_P, i64, i32, i64, i32, _P, ctypes.POINTER(optim_route_hp), _P, _P, _P], i32),
+            "optim_route_grad": ([_P, i64, i32, i64, i32, ctypes.POINTER(optim_route_hp), _P, _P, _P, i64, _P], i32),
+            "optim_step_route_bias": ([_P, i32, _P, _P, _P, _P], i32),
+            "optim_route_rows_workspace": ([i64, i32, i32, ctypes.POINTER(sz)], i32),
+            "optim_route_rows": ([_P, i64, i32, i32, _P, _P, _P, _P, sz, _P], i32),
+            "optim_expert_gather": ([_P, i64, i32, _P, _P, i64, i32, i64, _P, i64, i64, _P], i32),
+            "optim_expert_combine": ([_P, i64, i64, i32, _P, _P, i64, i32, i64, _P, i64, ctypes.POINTER(optim_dropout_hp), _P,
+                                      _P, i64, _P], i32),
+            "optim_expert_combine_grad": ([_P, i64, i32, _P, i64, i64, _P, _P, i64, i32, i64,
+                                           ctypes.POINTER(optim_dropout_hp), _P, _P, i64, _P, _P], i32),
+            "optim_dropout": ([_P, i32, i64, _P, ctypes.POINTER(optim_dropout_hp), _P, _P, _P], i32),
             "optim_expert_grad": ([_P, i64, _P, i64, i32, _P, i32, i64, i64, i64, _P, i32, i32, _P, _P, sz, _P], i32),
         }
         for name, (args, res) in sigs.items():
@@ -418,6 +452,157 @@ def optim_expert_grad(x, dy, offsets, dw, *, accumulate: bool = False, scale=Non
     _check(lib().optim_expert_grad(px, ldx, py, ldy, codes[x.dtype], _ptr(offsets), dw.size(0), x.size(0), x.size(1),
                                    dy.size(1), _ptr(dw), codes[dw.dtype], int(accumulate), _ptr(scale), _ptr(workspace),
                                    nbytes, _stream(stream)), "optim_expert_grad")
+
+
+# --------------------------------------------------------------------------
+# routing, the experts' rows, dropout (optim_route.h, optim_dropout.h)
+def _float_code(*tensors) -> int:
+    """The one dtype code of the tensors that are given."""
+    import torch
+    codes = {torch.float32: OPTIM_F32, torch.bfloat16: OPTIM_BF16, torch.float16: OPTIM_F16}
+    kinds = {t.dtype for t in tensors if t is not None}
+    if len(kinds) != 1 or not kinds <= set(codes):
+        raise ValueError(f"expected tensors of one type, float32, bfloat16 or float16, got {sorted(map(str, kinds))}")
+    return codes[kinds.pop()]
+
+
+def _expect(t, dtype: str, shape, what: str):
+    """Address of a contiguous tensor of that type and shape; None passes through."""
+    if t is None:
+        return None
+    if str(t.dtype) != "torch." + dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    return _ptr(t)
+
+
+def _scalar(t, dtype: str, what: str):
+    if t is None:
+        return None
+    if str(t.dtype) != "torch." + dtype or t.numel() != 1:
+        raise ValueError(f"{what}: expected one {dtype}, got {t.dtype} {tuple(t.shape)}")
+    return _ptr(t)
+
+
+def _by_ref(hp):
+    return ctypes.byref(hp) if hp is not None else None
+
+
+def optim_route(logits, hp: optim_route_hp, idx, weights, *, bias=None, stream=None) -> None:
+    """logits [tokens, experts] (rows may lie apart), idx int32 and weights
+    float32 [tokens, topk], bias float32 [experts]."""
+    code = _float_code(logits)
+    p, ld = _rows(logits, "logits")
+    t, e = logits.shape
+    _check(lib().optim_route(p, ld, code, t, e, _expect(bias, "float32", (e,), "bias"), ctypes.byref(hp),
+                             _expect(idx, "int32", (t, hp.topk), "idx"),
+                             _expect(weights, "float32", (t, hp.topk), "weights"), _stream(stream)), "optim_route")
+
+
+def optim_route_grad(logits, hp: optim_route_hp, idx, dweights, dlogits, *, stream=None) -> None:
+    """dlogits: type and shape of logits (rows of both may lie apart)."""
+    code = _float_code(logits, dlogits)
+    (p, ld), (pd, ldd) = _rows(logits, "logits"), _rows(dlogits, "dlogits")
+    if logits.shape != dlogits.shape:
+        raise ValueError(f"shapes do not fit: logits {tuple(logits.shape)}, dlogits {tuple(dlogits.shape)}")
+    t, e = logits.shape
+    _check(lib().optim_route_grad(p, ld, code, t, e, ctypes.byref(hp), _expect(idx, "int32", (t, hp.topk), "idx"),
+                                  _expect(dweights, "float32", (t, hp.topk), "dweights"), pd, ldd, _stream(stream)),
+           "optim_route_grad")
+
+
+def optim_step_route_bias(offsets, bias, rate, *, found_inf=None, stream=None) -> None:
+    """offsets int32 [experts + 1], bias float32 [experts], rate one float32."""
+    e = bias.numel()
+    _check(lib().optim_step_route_bias(_expect(offsets, "int32", (e + 1,), "offsets"), e,
+                                       _expect(bias, "float32", (e,), "bias"), _scalar(rate, "float32", "rate"),
+                                       _scalar(found_inf, "float32", "found_inf"), _stream(stream)),
+           "optim_step_route_bias")
+
+
+def optim_route_rows_workspace(tokens: int, topk: int, experts: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().optim_route_rows_workspace(int(tokens), int(topk), int(experts), ctypes.byref(out)),
+           "optim_route_rows_workspace")
+    return out.value
+
+
+def optim_route_rows(idx, offsets, place, *, order=None, workspace=None, stream=None) -> None:
+    """idx and place int32 [tokens, topk], offsets int32 [experts + 1], order
+    int32 [tokens * topk], workspace: a tensor of at least
+    optim_route_rows_workspace bytes."""
+    if idx.dim() != 2 or offsets.dim() != 1:
+        raise ValueError(f"shapes do not fit: idx {tuple(idx.shape)}, offsets {tuple(offsets.shape)}")
+    t, k = idx.shape
+    nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(lib().optim_route_rows(_expect(idx, "int32", (t, k), "idx"), t, k, offsets.numel() - 1,
+                                  _expect(offsets, "int32", (offsets.numel(),), "offsets"),
+                                  _expect(place, "int32", (t, k), "place"), _expect(order, "int32", (t * k,), "order"),
+                                  _ptr(workspace), nbytes, _stream(stream)), "optim_route_rows")
+
+
+def _token_shapes(by_token, by_row, place):
+    """(tokens, topk, dim, rows) of matrices by token and by row."""
+    sizes = [m.shape for m in (*by_token, *by_row) if m is not None]
+    if place.dim() != 2 or any(len(s) != 2 or s[1] != sizes[0][1] for s in sizes) or any(
+            m.shape[0] != place.shape[0] for m in by_token if m is not None) or len(
+            {m.shape[0] for m in by_row if m is not None}) != 1:
+        raise ValueError(f"shapes do not fit: {[tuple(s) for s in sizes]}, place {tuple(place.shape)}")
+    return place.shape[0], place.shape[1], sizes[0][1], [m for m in by_row if m is not None][0].shape[0]
+
+
+def optim_expert_gather(x, place, y, *, weights=None, stream=None) -> None:
+    """x [tokens, dim], y [rows, dim] of one type (rows may lie apart), place
+    int32 and weights float32 [tokens, topk]."""
+    code = _float_code(x, y)
+    t, k, dim, rows = _token_shapes((x,), (y,), place)
+    (px, ldx), (py, ldy) = _rows(x, "x"), _rows(y, "y")
+    _check(lib().optim_expert_gather(px, ldx, code, _expect(place, "int32", (t, k), "place"),
+                                     _expect(weights, "float32", (t, k), "weights"), t, k, dim, py, ldy, rows,
+                                     _stream(stream)), "optim_expert_gather")
+
+
+def optim_expert_combine(y, place, out, *, weights=None, residual=None, dropout: Optional[optim_dropout_hp] = None, step=None,
+                         stream=None) -> None:
+    """y [rows, dim], out and residual [tokens, dim] of one type (rows may lie
+    apart; out may be residual), place int32 and weights float32 [tokens, topk],
+    step one int32."""
+    code = _float_code(y, out, residual)
+    t, k, dim, rows = _token_shapes((out, residual), (y,), place)
+    (py, ldy), (po, ldo) = _rows(y, "y"), _rows(out, "out")
+    pr, ldr = _rows(residual, "residual") if residual is not None else (None, 0)
+    _check(lib().optim_expert_combine(py, ldy, rows, code, _expect(place, "int32", (t, k), "place"),
+                                      _expect(weights, "float32", (t, k), "weights"), t, k, dim, pr, ldr, _by_ref(dropout),
+                                      _scalar(step, "int32", "step"), po, ldo, _stream(stream)), "optim_expert_combine")
+
+
+def optim_expert_combine_grad(dout, y, place, dy, *, weights=None, dweights=None, dropout: Optional[optim_dropout_hp] = None,
+                              step=None, stream=None) -> None:
+    """dout [tokens, dim], y and dy [rows, dim] of one type (rows may lie apart;
+    dy may be y; y is read for dweights only; y or dy may be None), place int32,
+    weights and dweights float32 [tokens, topk], step one int32."""
+    code = _float_code(dout, y, dy)
+    if y is None and (dy is None or dweights is not None):
+        raise ValueError("dweights takes y, and without it there must be dy")
+    t, k, dim, rows = _token_shapes((dout,), (y, dy), place)
+    pd, ldd = _rows(dout, "dout")
+    py, ldy = _rows(y, "y") if y is not None else (None, 0)
+    pg, ldg = _rows(dy, "dy") if dy is not None else (None, 0)
+    _check(lib().optim_expert_combine_grad(pd, ldd, code, py, ldy, rows, _expect(place, "int32", (t, k), "place"),
+                                           _expect(weights, "float32", (t, k), "weights"), t, k, dim, _by_ref(dropout),
+                                           _scalar(step, "int32", "step"), pg, ldg,
+                                           _expect(dweights, "float32", (t, k), "dweights"), _stream(stream)),
+           "optim_expert_combine_grad")
+
+
+def optim_dropout(x, out, hp: optim_dropout_hp, *, residual=None, step=None, stream=None) -> None:
+    """x, out and residual of one type and number of elements (out may be either
+    of them), step one int32."""
+    code = _float_code(x, out, residual)
+    if out.numel() != x.numel() or (residual is not None and residual.numel() != x.numel()):
+        raise ValueError(f"sizes do not fit: x {tuple(x.shape)}, out {tuple(out.shape)}, residual "
+                         f"{None if residual is None else tuple(residual.shape)}")
+    _check(lib().optim_dropout(_ptr(x), code, x.numel(), _ptr(residual), ctypes.byref(hp), _scalar(step, "int32", "step"),
+                               _ptr(out), _stream(stream)), "optim_dropout")
 
 
 def optim_scaler_update(scale_dev, inv_scale_dev, growth_tracker_dev, found_inf_dev, growth_factor: float,

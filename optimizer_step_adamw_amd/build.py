@@ -18,8 +18,9 @@ LIB_PATH = os.path.join(LIB_DIR, "liboptim_step.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("kernels_adam.hip", "kernels_mini.hip", "kernels_blockwise.hip",
                                            "kernels_util.hip", "kernels_lion_lamb.hip", "kernels_scaled.hip",
                                            "kernels_grads.hip", "kernels_muon.hip", "kernels_muon_slab.hip",
-                                           "kernels_expert.hip",
-                                           "api.cpp")]
+                                           "kernels_expert.hip", "kernels_route.hip", "kernels_rows.hip",
+                                           "kernels_tokens.hip", "kernels_dropout.hip",
+                                           "api.cpp", "api_experts.cpp")]
 ARCH = os.environ.get("OPTIM_STEP_ARCH", "gfx950")
 
 

@@ -1,0 +1,62 @@
+// kernels_dropout.hip -- dropout from a counter (optim_dropout).
+//
+// A lane takes the elements of one block of the generator, eight neighbours whose
+// places begin at a multiple of eight: one call of the generator, 20 products of
+// 32 bits, for 16 bytes (16-bit types) read and written.
+#include "elems.h"
+
+namespace optim {
+namespace {
+
+template <int DT, bool RES>
+__global__ __launch_bounds__(kThreads) void dropout_kernel(const char *x, const char *res, char *out, int64_t n, DropArgs d) {
+    const uint32_t step = drop_step(d);
+    const int64_t lead = d.first & 7;  // places of the first block that lie before element 0
+    const int64_t blocks = (lead + n + 7) >> 3;
+    for (int64_t b = (int64_t)blockIdx.x * kThreads + threadIdx.x; b < blocks; b += (int64_t)gridDim.x * kThreads) {
+        const int64_t e = b * 8 - lead;
+        const Words w = philox((uint64_t)((d.first >> 3) + b), step, d.site, d.seed);
+        if (e >= 0 && e + 8 <= n) {
+            float v[8], r[8];
+            floats<DT>(load8<DT>(x + e * kElem<DT>), v);
+            if constexpr (RES) floats<DT>(load8<DT>(res + e * kElem<DT>), r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[i] = draw_of(w, i) < d.bar ? 0.0f : v[i] * d.scale;
+                if constexpr (RES) v[i] = r[i] + v[i];
+            }
+            store8<DT>(out + e * kElem<DT>, rounded<DT>(v));
+            continue;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {  // the first or the last block
+            if (e + i < 0 || e + i >= n) continue;
+            float v = draw_of(w, i) < d.bar ? 0.0f : element<DT>(x + (e + i) * kElem<DT>) * d.scale;
+            if constexpr (RES) v = element<DT>(res + (e + i) * kElem<DT>) + v;
+            put_element<DT>(out + (e + i) * kElem<DT>, v);
+        }
+    }
+}
+
+template <int DT>
+hipError_t launch_dropout_t(const char *x, const char *residual, char *out, int64_t n, const DropArgs &d, hipStream_t s) {
+    const int64_t blocks = (n + 14) / 8;
+    const int64_t g = (blocks + kThreads - 1) / kThreads;
+    const dim3 grid((unsigned)(g < (1 << 23) ? g : 1 << 23));
+    if (residual)
+        hipLaunchKernelGGL((dropout_kernel<DT, true>), grid, dim3(kThreads), 0, s, x, residual, out, n, d);
+    else
+        hipLaunchKernelGGL((dropout_kernel<DT, false>), grid, dim3(kThreads), 0, s, x, residual, out, n, d);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_dropout(const char *x, const char *residual, char *out, int64_t n, const DropArgs &d, int dtype,
+                          hipStream_t s) {
+    if (dtype == OPTIM_F32) return launch_dropout_t<OPTIM_F32>(x, residual, out, n, d, s);
+    if (dtype == OPTIM_BF16) return launch_dropout_t<OPTIM_BF16>(x, residual, out, n, d, s);
+    return launch_dropout_t<OPTIM_F16>(x, residual, out, n, d, s);
+}
+
+}  // namespace optim
