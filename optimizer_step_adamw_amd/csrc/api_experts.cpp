@@ -213,8 +213,7 @@ int optim_route_rows_workspace(int64_t tokens, int32_t topk, int32_t experts, si
     if (!bytes) return fail(OPTIM_EINVAL, "bytes is NULL");
     if (const int rc = check_experts(experts)) return rc;
     if (const int rc = check_choices(tokens, topk)) return rc;
-    const RowsShape s = rows_shape(tokens * topk);
-    *bytes = s.blocks > 1 ? (size_t)s.blocks * ((size_t)experts + 1) * 4 : 0;
+    *bytes = rows_workspace(rows_shape(tokens * topk), experts);
     return OPTIM_OK;
 } OPTIM_CATCH
 
@@ -228,7 +227,7 @@ int optim_route_rows(const int32_t *idx_dev, int64_t tokens, int32_t topk, int32
     if (!aligned(idx_dev, 4) || !aligned(offsets_dev, 4) || !aligned(place_dev, 4) || !aligned(order_dev, 4))
         return fail(OPTIM_EALIGN, "buffer misaligned");
     const RowsShape shape = rows_shape(n);
-    const size_t need = shape.blocks > 1 ? (size_t)shape.blocks * ((size_t)experts + 1) * 4 : 0;
+    const size_t need = rows_workspace(shape, experts);
     if (need) {
         if (!workspace || !aligned(workspace, 256))
             return fail(OPTIM_EWORKSPACE, "workspace must be a 256-byte aligned device pointer");

@@ -11,6 +11,7 @@ namespace {
 
 typedef u32x4 __attribute__((aligned(2))) u32x4_at2;
 typedef u32x4 __attribute__((aligned(4))) u32x4_at4;
+typedef u32x2 __attribute__((aligned(2))) u32x2_at2;
 
 // DT: OPTIM_F32, OPTIM_BF16 or OPTIM_F16
 template <int DT>

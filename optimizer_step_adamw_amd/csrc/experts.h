@@ -43,7 +43,7 @@ hipError_t launch_route_bias(const int32_t *offsets, int32_t experts, float *bia
 struct RowsArgs {
     const int32_t *idx;
     int32_t *offsets, *place, *order;  // order or NULL
-    int32_t *counts;                   // [blocks][experts + 1], NULL where one block does it all
+    int32_t *counts;                   // [blocks], rows_workspace() bytes; NULL where one block does it all
     int32_t n, experts, chunk, blocks;
 };
 // Choices a workgroup takes, a multiple of 512, and workgroups.
@@ -51,6 +51,7 @@ struct RowsShape {
     int32_t chunk, blocks;
 };
 RowsShape rows_shape(int64_t n);
+size_t rows_workspace(RowsShape shape, int32_t experts);
 hipError_t launch_rows(const RowsArgs &a, hipStream_t s);
 
 // Matrices of `dim` columns; distances in bytes.
