@@ -206,6 +206,29 @@ __device__ __forceinline__ uint32_t dpp(uint32_t x) {
 }
 template <int CTRL>
 __device__ __forceinline__ float dpp(float x) { return __uint_as_float(dpp<CTRL>(__float_as_uint(x))); }
+// The largest and smallest of numbers that are no NaN (fmaxf and fminf quiet
+// each argument first).
+__device__ __forceinline__ float most_of(float x, float y, float z) {
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(x), "v"(y), "v"(z));
+    return r;
+}
+__device__ __forceinline__ float least_of(float x, float y, float z) {
+    float r;
+    asm("v_min3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(x), "v"(y), "v"(z));
+    return r;
+}
+__device__ __forceinline__ float more_of(float x, float y) {
+    float r;
+    asm("v_max_f32 %0, %1, %2" : "=v"(r) : "v"(x), "v"(y));
+    return r;
+}
+__device__ __forceinline__ float less_of(float x, float y) {
+    float r;
+    asm("v_min_f32 %0, %1, %2" : "=v"(r) : "v"(x), "v"(y));
+    return r;
+}
+
 template <class T, class F>
 __device__ __forceinline__ T join16(T x, F &&f) {
     x = f(x, dpp<kXor1>(x));
@@ -213,16 +236,16 @@ __device__ __forceinline__ T join16(T x, F &&f) {
     x = f(x, dpp<kMirror8>(x));
     return f(x, dpp<kMirror16>(x));
 }
-__device__ __forceinline__ float max16(float x) { return join16(x, [](float a, float b) { return fmaxf(a, b); }); }
-__device__ __forceinline__ float min16(float x) { return join16(x, [](float a, float b) { return fminf(a, b); }); }
+__device__ __forceinline__ float max16(float x) { return join16(x, [](float a, float b) { return more_of(a, b); }); }
+__device__ __forceinline__ float min16(float x) { return join16(x, [](float a, float b) { return less_of(a, b); }); }
 __device__ __forceinline__ float sum16(float x) { return join16(x, [](float a, float b) { return a + b; }); }
 
-// f(number, value of that lane) for each lane of the 16
+// f(number, value of that lane) for every by-th lane of the 16, by a power of two
 template <int I = 0, class F>
-__device__ __forceinline__ void each16(float x, F &&f) {
+__device__ __forceinline__ void each16(int32_t by, float x, F &&f) {
     if constexpr (I < 16) {
-        f(I, dpp<kBroadcast + I>(x));
-        each16<I + 1>(x, f);
+        if (!(I & (by - 1))) f(I, dpp<kBroadcast + I>(x));
+        each16<I + 1>(by, x, f);
     }
 }
 
@@ -283,42 +306,76 @@ __device__ __forceinline__ void absorb_lane(uint32_t (&a)[D]) {
 struct Lay {
     int32_t n;
     bool quads;  // four neighbours are one access, all there or none
+    bool full;   // every one of the V of every lane is there
 };
-template <int V, int DT>
-__device__ __forceinline__ void load_row(const char *row, int32_t experts, Lay lay, int lane, float (&l)[V], bool &nan) {
-    const int32_t e0 = lane * lay.n;
-    float raw[V];
-    if (lay.quads) {
+template <int DT>
+__device__ __forceinline__ void load4(const char *p, float *x) {
+    if constexpr (DT == OPTIM_F32) {
+        const u32x4 u = *(const GMEM u32x4_at4 *)gp(p);
 #pragma unroll
-        for (int q = 0; q < V / 4; ++q) {
-            const bool in = q * 4 < lay.n && e0 + q * 4 < experts;
-            const char *p = row + (int64_t)(in ? e0 + q * 4 : 0) * kElem<DT>;
-            if constexpr (DT == OPTIM_F32) {
-                const u32x4 u = *(const GMEM u32x4_at4 *)gp(p);
+        for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(u[i]);
+    } else {
+        const u32x2 u = *(const GMEM u32x2_at2 *)gp(p);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) raw[q * 4 + i] = in ? __uint_as_float(u[i]) : -INFINITY;
-            } else {
-                const u32x2 u = *(const GMEM u32x2_at2 *)gp(p);
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (DT == OPTIM_BF16) x[i] = __uint_as_float(i % 2 ? u[i / 2] & 0xFFFF0000u : u[i / 2] << 16);
+            else x[i] = f16_to_f32(u[i / 2] >> (i % 2 * 16) & 0xFFFFu);
+        }
+    }
+}
+// This lane's part of a row, `none` where there is no expert.
+template <int V, int DT, bool FULL>
+__device__ __forceinline__ void load_row(const char *row, int32_t experts, Lay lay, int lane, float none, float (&x)[V]) {
+    const int32_t e0 = lane * (FULL ? V : lay.n);
+    if (FULL || lay.quads) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t h = u[i / 2] >> (i % 2 * 16) & 0xFFFFu;
-                    raw[q * 4 + i] = !in ? -INFINITY : DT == OPTIM_BF16 ? bf16_to_f32(h) : f16_to_f32(h);
-                }
-            }
+        for (int q = 0; q < V; q += 4) {
+            const bool in = FULL || (q < lay.n && e0 + q < experts);
+            load4<DT>(row + (int64_t)(in ? e0 + q : 0) * kElem<DT>, x + q);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (!FULL) x[q + i] = in ? x[q + i] : none;
         }
     } else {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const bool in = v < lay.n && e0 + v < experts;
-            const float x = logit_at<DT>(row, in ? e0 + v : 0);
-            raw[v] = in ? x : -INFINITY;
+            x[v] = logit_at<DT>(row, in ? e0 + v : 0);
+            x[v] = in ? x[v] : none;
         }
     }
+}
+
+// Whether a sum of the numbers is finite in every lane: then so are they.
+template <int V>
+__device__ __forceinline__ bool all_finite(const float (&x)[V]) {
+    float s = x[0];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        nan |= raw[v] != raw[v];
-        l[v] = tamed(raw[v]);
+    for (int v = 1; v < V; ++v) s += x[v];
+    return !__any(!(fabsf(s) < INFINITY));
+}
+
+// The whole part; 0 of what is negative, -inf or NaN (which the language leaves
+// open, and the instruction does not).
+__device__ __forceinline__ uint32_t whole_part(float x) {
+    uint32_t u;
+    asm("v_cvt_u32_f32 %0, %1" : "=v"(u) : "v"(x));
+    return u;
+}
+
+// x[at], at below N, from registers
+template <int N>
+__device__ __forceinline__ uint32_t pick(const uint32_t (&x)[N], int at) {
+    uint32_t y[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) y[i] = x[i];
+#pragma unroll
+    for (int s = 1; s < N; s *= 2) {
+        const bool odd = at & s;
+#pragma unroll
+        for (int i = 0; i < N; i += 2 * s) y[i] = odd ? y[i + s] : y[i];
     }
+    return y[0];
 }
 
 // Sixteen lanes a token, V experts a lane, the D largest choices (topk <= D).
@@ -339,16 +396,18 @@ __device__ __forceinline__ void load_row(const char *row, int32_t experts, Lay l
 // from the sum (V + 4 terms one after another, V <= 64: 68) and 3 of itself,
 // below (V + 32) s as |x| e^-x < 1; the sum with b half of itself.  Twice that is
 // allowed for.
-template <int V, int D, int DT>
+template <int V, int D, int DT, bool FULL>
 __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, Lay lay) {
     constexpr int V64 = V < 4 ? 1 : V / 4;
     constexpr int kBits = V == 4 ? 6 : V == 8 ? 7 : V == 16 ? 8 : V == 32 ? 9 : 10;  // of an expert's number
     constexpr uint32_t kNumber = (1u << kBits) - 1;
     constexpr float kSteps = (float)((1 << (kBits < 8 ? 24 : 32 - kBits)) - 8);
+    constexpr float kLog2e = 1.44269504f;
     __shared__ double lds[kWaves][64 * V64];
     const int lane = threadIdx.x & 63, l16 = lane & 15, wave = threadIdx.x >> 6;
     const bool sums = a.groups > 1 && a.group_best > 1, scored = a.bias || sums;
-    const int32_t e0 = l16 * lay.n;
+    const bool whole = DT != OPTIM_F32 && !scored;  // exact keys
+    const int32_t e0 = l16 * (FULL ? V : lay.n);
     const int64_t t0 = ((int64_t)blockIdx.x * kWaves + wave) * 4;
     if (t0 >= a.tokens) return;
     uint64_t redo;
@@ -356,74 +415,100 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, Lay lay) {
         const int64_t t = t0 + (lane >> 4);
         const bool live = t < a.tokens;
         const char *row = a.logits + (live ? t : t0) * a.ldl;
-        float c[V];
-        bool nan = false;
-        load_row<V, DT>(row, a.experts, lay, l16, c, nan);
+        float c[V], b[V];
+        load_row<V, DT, FULL>(row, a.experts, lay, l16, -INFINITY, c);
+        if (a.bias) load_row<V, OPTIM_F32, FULL>(reinterpret_cast<const char *>(a.bias), a.experts, lay, l16, -INFINITY, b);
+        // (in every lane) some expert may not be available
+        bool masked = !FULL || !all_finite(c), nan = false;
+        if (masked) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                nan |= c[v] != c[v];
+                c[v] = tamed(c[v]);
+            }
+        }
         // ---- scores, where they count
         const bool soft = a.score == OPTIM_ROUTE_SOFTMAX;
         float most = -INFINITY, total = 1.0f, error = 0.0f;
         if (soft && (scored || !a.renormalise)) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) most = fmaxf(most, c[v]);
+            for (int v = 0; v < V; v += 2) most = most_of(most, c[v], c[v + 1]);
             most = max16(most);
             total = 0.0f;
             const float from = most > -INFINITY ? most : 0.0f;
             if (!scored) {
 #pragma unroll
-                for (int v = 0; v < V; ++v) total += __builtin_amdgcn_exp2f((c[v] - from) * 1.44269504f);
+                for (int v = 0; v < V; ++v) total += __builtin_amdgcn_exp2f((c[v] - from) * kLog2e);
                 total = sum16(total);
             } else {
                 float s[V];
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    s[v] = __builtin_amdgcn_exp2f((c[v] - from) * 1.44269504f);
+                    s[v] = __builtin_amdgcn_exp2f((c[v] - from) * kLog2e);
                     total += s[v];
                 }
                 total = sum16(total);
                 const float inv = total > 0.0f ? __builtin_amdgcn_rcpf(total) : 0.0f;
                 error = (2.0f * (V + 32)) * inv;
+                if (masked) {
 #pragma unroll
-                for (int v = 0; v < V; ++v) c[v] = c[v] > -INFINITY ? s[v] * inv : -INFINITY;
+                    for (int v = 0; v < V; ++v) c[v] = c[v] > -INFINITY ? s[v] * inv : -INFINITY;
+                } else {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) c[v] = s[v] * inv;
+                }
             }
         } else if (scored) {
             error = 8.0f;
+            if (masked) {
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                c[v] = c[v] > -INFINITY ? __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(c[v] * -1.44269504f)) : -INFINITY;
+                for (int v = 0; v < V; ++v)
+                    c[v] = c[v] > -INFINITY ? __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(c[v] * -kLog2e)) : -INFINITY;
+            } else {
+#pragma unroll
+                for (int v = 0; v < V; ++v) c[v] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(c[v] * -kLog2e));
+            }
         }
         if (a.bias) {
+            if (!FULL || !all_finite(b)) {
+                masked = true;
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float b = a.bias[v < lay.n && e0 + v < a.experts ? e0 + v : 0];
-                c[v] = b > -INFINITY ? c[v] + b : -INFINITY;
+                for (int v = 0; v < V; ++v) b[v] = tamed(b[v]);
             }
+#pragma unroll
+            for (int v = 0; v < V; ++v) c[v] += b[v];
         }
         // ---- the row's range
         float hi = -INFINITY, lo = INFINITY;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            hi = fmaxf(hi, c[v]);
-            lo = fminf(lo, c[v] > -INFINITY ? c[v] : INFINITY);
+        for (int v = 0; v < V; v += 2) hi = most_of(hi, c[v], c[v + 1]);
+        if (masked) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) lo = fminf(lo, c[v] > -INFINITY ? c[v] : INFINITY);
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; v += 2) lo = least_of(lo, c[v], c[v + 1]);
         }
         hi = max16(hi);
         lo = min16(lo);
-        bool again = scored && !(hi < INFINITY) && hi > -INFINITY;  // an infinite bias
-        const bool flat = hi == lo;
         error = scored ? (error + 2.0f * fmaxf(fabsf(hi), fabsf(lo))) * 0x1p-24f : 0.0f;
-        const float floor = fmaxf(lo, hi - 32.0f);  // choices far below the largest are one
-        const float step = hi > floor ? kSteps / (hi - floor) : 0.0f;
-        // ---- keys, sorted
+        const float floor = fmaxf(lo, hi - 32.0f);  // choices far below the largest have no place
+        const float step = hi > floor ? fminf(kSteps * __builtin_amdgcn_rcpf(hi - floor), FLT_MAX) : 1.0f;
+        // ---- keys: place and number, at first the number within the lane; no place
+        // (0) for what is not available
         uint32_t key[V];
+        const uint32_t number = kNumber - (uint32_t)e0 - (V - 1);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             uint32_t place;
-            if (DT != OPTIM_F32 && !scored) {
-                const uint32_t u = __float_as_uint(c[v] + 0.0f);  // (-0 is 0)
+            if (whole) {
+                const uint32_t u = __float_as_uint(c[v] + 0.0f);  // (-0 is 0; of -inf below 2^10)
                 place = (u ^ (uint32_t)((int32_t)u >> 31 | INT32_MIN)) >> 13;
+                place = c[v] > -INFINITY ? place : 0u;
             } else {
-                place = (uint32_t)(fmaxf(c[v] - floor, 0.0f) * step);
+                place = whole_part(__builtin_fmaf(c[v] - floor, step, 1.0f));
             }
-            key[v] = c[v] > -INFINITY ? (place + 1u) << kBits | (kNumber - (uint32_t)(e0 + v)) : 0u;
+            key[v] = place << kBits | (uint32_t)(V - 1 - v);
         }
         uint32_t best[D];
 #pragma unroll
@@ -439,72 +524,78 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, Lay lay) {
                 absorb<D>(best, more);
             }
         }
+#pragma unroll
+        for (int i = 0; i < D; ++i) best[i] += number;
         // ---- groups: 16 / groups lanes each
+        bool again = false, kept = true;
         if (a.groups > 1) {
             float b0 = -INFINITY, b1 = -INFINITY;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 b1 = __builtin_amdgcn_fmed3f(c[v], b0, b1);
-                b0 = fmaxf(b0, c[v]);
+                b0 = more_of(b0, c[v]);
             }
             auto with = [&](float o0, float o1) {
-                b1 = fmaxf(fminf(b0, o0), fmaxf(b1, o1));
-                b0 = fmaxf(b0, o0);
+                b1 = most_of(less_of(b0, o0), b1, o1);
+                b0 = more_of(b0, o0);
             };
             if (a.groups <= 8) with(dpp<kXor1>(b0), dpp<kXor1>(b1));
             if (a.groups <= 4) with(dpp<kXor2>(b0), dpp<kXor2>(b1));
             if (a.groups <= 2) with(dpp<kMirror8>(b0), dpp<kMirror8>(b1));
             const float mine = sums && b1 > -INFINITY ? b0 + b1 : b0;
-            const int32_t lanes = 16 / a.groups, first = l16 / lanes * lanes;
-            const float apart = scored ? 4.0f * error : 0.0f;
-            int32_t above = 0, near = 0;  // lanes of groups ahead for certain; and of those that may be
+            const int32_t lanes = 16 / a.groups, first = l16 & -lanes;
+            const float apart = 4.0f * error;
+            int32_t above = 0, near = 0;  // groups ahead for certain; and those that may be
             if (scored) {
-                each16(mine, [&](int, float r) {
-                    above += r > mine + apart;
-                    near += r >= mine - apart;
+                const float up = mine + apart, down = mine - apart;
+                each16(lanes, mine, [&](int, float r) {
+                    above += r > up;
+                    near += r >= down;
                 });
-                near -= lanes;
+                near -= mine > -INFINITY ? 1 : a.groups;  // itself
             } else {
-                each16(mine, [&](int i, float r) { above += r > mine || (r == mine && i < first); });
-                near = above;
+                each16(lanes, mine, [&](int i, float r) { near += (r > mine) | ((r == mine) & (i < first)); });
             }
-            const int32_t bar = a.top_groups * lanes;
-            const bool kept = near < bar;
-            again |= !kept && above < bar && mine > -INFINITY;
+            kept = near < a.top_groups;
+            again = scored && !kept && above < a.top_groups && mine > -INFINITY;
 #pragma unroll
             for (int i = 0; i < D; ++i) best[i] = kept ? best[i] : 0u;
-#pragma unroll
-            for (int v = 0; v < V; ++v) key[v] = kept ? key[v] : 0u;
         }
         absorb_lane<D, kXor1>(best);
         absorb_lane<D, kXor2>(best);
         absorb_lane<D, kMirror8>(best);
         absorb_lane<D, kMirror16>(best);
         // ---- lane j takes choice j; are neighbours far enough apart?
-        uint32_t taken = 0u;
-#pragma unroll
-        for (int i = 0; i < D; ++i) taken = l16 == i ? best[i] : taken;
-        if (!(DT != OPTIM_F32 && !scored)) {
+        const uint32_t taken = pick<D>(best, l16 & (D - 1));
+        const bool mine_is = l16 < a.topk, placed = taken >> kBits;
+        if (!whole) {
+            const float far = 2.0f * error * step + 2.0f;  // steps
+            const uint32_t margin = !scored ? 1u << kBits : far < (float)(1u << (30 - kBits)) ? ((uint32_t)far + 1u) << kBits : 1u << 30;
             uint32_t next = dpp<kNext>(taken);
             if (V < 64 && a.topk == D) {
-                uint32_t behind = 0u;
+                const uint32_t last = best[D - 1] - 1u - number;
+                uint32_t behind = ~0u;
 #pragma unroll
-                for (int v = 0; v < V; ++v) behind = key[v] < best[D - 1] && key[v] > behind ? key[v] : behind;
-                behind = join16(behind, [](uint32_t x, uint32_t y) { return x > y ? x : y; });
-                next = l16 == D - 1 ? behind : next;
+                for (int v = 0; v < V; ++v) behind = last - key[v] < behind ? last - key[v] : behind;
+                behind = kept ? behind : ~0u;
+                behind = join16(behind, [](uint32_t x, uint32_t y) { return x < y ? x : y; });
+                next = l16 == D - 1 ? best[D - 1] - 1u - behind : next;
             }
-            const float least = 2.0f * error * step + 2.0f;  // steps
-            const uint32_t margin = !scored ? 0u : least < 1e9f ? (uint32_t)least : 1u << 30;
-            again |= l16 < a.topk && next && !(flat && !scored) && (taken >> kBits) - (next >> kBits) <= margin;
+            // equal logits are one choice whose order the numbers give
+            again |= mine_is && placed && next >> kBits && taken - next < margin && !(hi == lo && !scored);
+            again |= mine_is && !placed && lo < floor;
         }
-        int32_t e = l16 < a.topk && taken ? (int32_t)(kNumber - (taken & kNumber)) : -1;
+        const int32_t e = mine_is && placed ? (int32_t)(kNumber - (taken & kNumber)) : -1;
         redo = __ballot(again && live);
         const bool sure = !(redo >> (lane & 48) & 0xFFFFull);
         // ---- weights
         const float mine = e >= 0 ? tamed(logit_at<DT>(row, e)) : -INFINITY;
         float w;
         if (a.renormalise) {
-            w = part_of_score(a.score, mine, max16(mine));
+            if (!soft && !__any(mine < -16.0f && e >= 0))  // (off by 28 x 2^-24 at most)
+                w = e >= 0 ? __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(mine * -kLog2e)) : 0.0f;
+            else
+                w = part_of_score(a.score, mine, max16(mine));
             total = sum16(w);
         } else if (soft) {
             w = e >= 0 ? expf(mine - most) : 0.0f;
@@ -515,7 +606,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, Lay lay) {
         w *= a.scale;
         const uint64_t nans = __ballot(nan);
         if (nans >> (lane & 48) & 0xFFFFull) w = __builtin_nanf("");
-        if (live && sure && l16 < a.topk) {
+        if (live && sure && mine_is) {
             a.idx[t * a.topk + l16] = e;
             a.weights[t * a.topk + l16] = w;
         }
@@ -528,95 +619,141 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, Lay lay) {
     }
 }
 
-template <int V, int DT>
+// ---------------------------------------------------------------- the gradient
+// L lanes a token (16, or 64 for more than 16 choices), lane j with choice j.  A
+// row passes through registers in chunks of eight, chunk c in lane c mod L, and
+// through LDS, where the chosen experts' terms join it.  Only the gradient of the
+// whole softmax (WHOLE) reads the row.
+template <int L>
+__device__ __forceinline__ float lanes_max(float x) { return L == 16 ? max16(x) : wave_max(x); }
+template <int L>
+__device__ __forceinline__ float lanes_sum(float x) { return L == 16 ? sum16(x) : wave_sum(x); }
+
+template <int L, int C, int DT, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void route_grad_kernel(RouteGradArgs a) {
-    __shared__ float lds[kWaves][64 * V];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    float *grad = lds[wave];
-    for (int64_t t = (int64_t)blockIdx.x * kWaves + wave; t < a.tokens; t += (int64_t)gridDim.x * kWaves) {
-        const char *row = a.logits + t * a.ldl;
-        const int32_t e = lane < a.topk ? a.idx[t * a.topk + lane] : -1;
-        const bool chosen = (uint32_t)e < (uint32_t)a.experts;
-        const float g = chosen ? a.dweights[t * a.topk + lane] * a.scale : 0.0f;
-        const float mine = chosen ? tamed(logit_at<DT>(row, e)) : -INFINITY;
-        float base[V];  // of every expert
-        float d = 0.0f; // of the chosen one beside
+    constexpr int kTokens = 64 / L;  // of a wavefront
+    __shared__ __align__(16) float lds[kWaves][kTokens][C * L * 8];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane & (L - 1);
+    const int64_t t0 = ((int64_t)blockIdx.x * kWaves + wave) * kTokens;
+    if (t0 >= a.tokens) return;
+    const int64_t t = t0 + lane / L;
+    const bool live = t < a.tokens;
+    float *grad = lds[wave][lane / L];
+    const char *row = a.logits + (live ? t : t0) * a.ldl;
+    const bool slot = live && l < a.topk;
+    const int32_t e = slot ? a.idx[t * a.topk + l] : -1;
+    const bool chosen = (uint32_t)e < (uint32_t)a.experts;
+    Raw8<DT> raw[C];
+    if constexpr (WHOLE) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) base[v] = 0.0f;
-        if (a.score == OPTIM_ROUTE_SOFTMAX && !a.renormalise) {
-            float l[V], most = -INFINITY, total = 0.0f;
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int32_t x = lane + 64 * v;
-                l[v] = x < a.experts ? tamed(logit_at<DT>(row, x)) : -INFINITY;
-                most = fmaxf(most, l[v]);
-            }
-            most = wave_max(most);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                l[v] = l[v] > -INFINITY ? expf(l[v] - most) : 0.0f;
-                total += l[v];
-            }
-            total = wave_sum(total);
-            const float inv = total > 0.0f ? 1.0f / total : 0.0f;
-            const float s = mine > -INFINITY ? expf(mine - most) * inv : 0.0f;
-            const float dot = wave_sum(g * s);
-#pragma unroll
-            for (int v = 0; v < V; ++v) base[v] = -(l[v] * inv) * dot;
-            d = g * s;
-        } else if (a.score == OPTIM_ROUTE_SIGMOID && !a.renormalise) {
-            d = g * sigmoid(mine) * sigmoid(-mine);
-        } else {
-            const float s = part_of_score(a.score, mine, wave_max(mine));
-            const float total = wave_sum(s);
-            const float w = total > 0.0f ? s / total : 0.0f;
-            const float dot = wave_sum(g * w);
-            d = w * (g - dot);
-            if (a.score == OPTIM_ROUTE_SIGMOID) d = d * sigmoid(-mine);
+        for (int i = 0; i < C; ++i) {
+            const int32_t first = (i * L + l) * 8, n = a.experts - first;
+            if (n > 0) raw[i] = get8<DT>(row + (int64_t)first * kElem<DT>, n);
         }
-        if (!(mine > -INFINITY)) d = 0.0f;
-        // of an expert named twice, the first name's lane writes the sum
-        bool first = chosen;
+    }
+    const float g = chosen ? a.dweights[t * a.topk + l] * a.scale : 0.0f;
+    const float mine = chosen ? tamed(logit_at<DT>(row, e)) : -INFINITY;
+    // Which of the lanes that name an expert comes first?  Each leaves its number.
+    if (chosen) reinterpret_cast<int32_t *>(grad)[e] = l;
+    wave_sync();
+    const bool twice = __any(chosen && reinterpret_cast<const int32_t *>(grad)[chosen ? e : 0] != l);
+    wave_sync();
+    float d;             // of the chosen expert, beside the row's own
+    float x[C][8];       // the row's own
+    if constexpr (WHOLE) {
+        float most = -INFINITY, total = 0.0f;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const int32_t n = a.experts - (i * L + l) * 8;
+            floats<DT>(raw[i], x[i]);
+#pragma unroll
+            for (int v = 0; v < 8; ++v) {
+                x[i][v] = v < n ? tamed(x[i][v]) : -INFINITY;
+                most = more_of(most, x[i][v]);
+            }
+        }
+        most = lanes_max<L>(most);
+        const float from = most > -INFINITY ? most : 0.0f;
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+#pragma unroll
+            for (int v = 0; v < 8; ++v) {
+                x[i][v] = __builtin_amdgcn_exp2f((x[i][v] - from) * 1.44269504f);
+                total += x[i][v];
+            }
+        total = lanes_sum<L>(total);
+        const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+        const float s = mine > -INFINITY ? expf(mine - from) * inv : 0.0f;
+        d = g * s;
+        const float by = -(lanes_sum<L>(d) * inv);
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+#pragma unroll
+            for (int v = 0; v < 8; ++v) x[i][v] = x[i][v] * by;
+    } else if (a.renormalise) {
+        const float s = part_of_score(a.score, mine, lanes_max<L>(mine));
+        const float total = lanes_sum<L>(s);
+        const float w = total > 0.0f ? s / total : 0.0f;
+        d = w * (g - lanes_sum<L>(g * w));
+        if (a.score == OPTIM_ROUTE_SIGMOID) d = d * sigmoid(-mine);
+    } else {
+        d = g * sigmoid(mine) * sigmoid(-mine);
+    }
+    if (!(mine > -INFINITY)) d = 0.0f;
+    bool first = chosen;
+    if (twice) {  // the first name's lane adds them up, in order
         float sum = d;
         for (int32_t j = 0; j < a.topk; ++j) {
-            const int32_t e2 = __shfl(e, j);
-            const float d2 = __shfl(d, j);
-            if (e2 != e || j == lane) continue;
-            if (j < lane) first = false;
+            const int32_t e2 = __shfl(e, (lane & -L) + j);
+            const float d2 = __shfl(d, (lane & -L) + j);
+            if (e2 != e || j == l) continue;
+            if (j < l) first = false;
             else sum += d2;
         }
+        d = sum;
+    }
 #pragma unroll
-        for (int v = 0; v < V; ++v) grad[lane + 64 * v] = base[v];
-        wave_sync();
-        if (first) grad[e] += sum;
-        wave_sync();
+    for (int i = 0; i < C; ++i) {
+        const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+        f32x4 *to = reinterpret_cast<f32x4 *>(grad + (i * L + l) * 8);
+        to[0] = WHOLE ? f32x4{x[i][0], x[i][1], x[i][2], x[i][3]} : zero;
+        to[1] = WHOLE ? f32x4{x[i][4], x[i][5], x[i][6], x[i][7]} : zero;
+    }
+    wave_sync();
+    if (first) grad[e] += d;
+    wave_sync();
+    if (!live) return;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int32_t x = lane + 64 * v;
-            if (x < a.experts) put_element<DT>(a.dlogits + t * a.ldd + (int64_t)x * kElem<DT>, grad[x]);
-        }
-        wave_sync();
+    for (int i = 0; i < C; ++i) {
+        const int32_t at = (i * L + l) * 8, n = a.experts - at;
+        if (n <= 0) continue;
+        const f32x4 *from = reinterpret_cast<const f32x4 *>(grad + at);
+        const f32x4 lo = from[0], hi = from[1];
+        const float y[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        put8<DT>(a.dlogits + t * a.ldd + (int64_t)at * kElem<DT>, n, rounded<DT>(y));
     }
 }
 
 // A launch takes fewer than 2^32 lanes: calls f(arguments of at most 2^25 tokens).
-template <class F>
-hipError_t route_slices(const RouteArgs &args, F &&f) {
-    constexpr int64_t kMost = int64_t(1) << 25;
-    RouteArgs a = args;
-    for (int64_t left = args.tokens; left > 0; left -= kMost) {
-        a.tokens = left < kMost ? left : kMost;
+constexpr int64_t kMostTokens = int64_t(1) << 25;
+void advance(RouteArgs &a) {
+    a.logits += kMostTokens * a.ldl;
+    a.idx += kMostTokens * a.topk;
+    a.weights += kMostTokens * a.topk;
+}
+void advance(RouteGradArgs &a) {
+    a.logits += kMostTokens * a.ldl;
+    a.idx += kMostTokens * a.topk;
+    a.dweights += kMostTokens * a.topk;
+    a.dlogits += kMostTokens * a.ldd;
+}
+template <class A, class F>
+hipError_t route_slices(A a, F &&f) {
+    for (int64_t left = a.tokens; left > 0; left -= kMostTokens, advance(a)) {
+        a.tokens = left < kMostTokens ? left : kMostTokens;
         f(a);
-        a.logits += kMost * a.ldl;
-        a.idx += kMost * a.topk;
-        a.weights += kMost * a.topk;
     }
     return hipGetLastError();
-}
-
-unsigned route_grid(int64_t tokens) {
-    const int64_t g = (tokens + kWaves - 1) / kWaves;
-    return (unsigned)(g < (1 << 23) ? g : 1 << 23);
 }
 
 template <int V>
@@ -629,15 +766,20 @@ void launch_route_wave(const RouteArgs &a, int dtype, hipStream_t s) {
     else
         hipLaunchKernelGGL((route_wave_kernel<V, OPTIM_F16>), grid, dim3(kThreads), 0, s, a);
 }
+template <int V, int D, int DT>
+void launch_route_t(const RouteArgs &a, Lay lay, hipStream_t s) {
+    const dim3 grid((unsigned)((a.tokens + kWaves * 4 - 1) / (kWaves * 4)));
+    if (lay.full)
+        hipLaunchKernelGGL((route_kernel<V, D, DT, true>), grid, dim3(kThreads), 0, s, a, lay);
+    else
+        hipLaunchKernelGGL((route_kernel<V, D, DT, false>), grid, dim3(kThreads), 0, s, a, lay);
+}
 template <int V, int D>
 void launch_route_d(const RouteArgs &a, Lay lay, int dtype, hipStream_t s) {
-    const dim3 grid((unsigned)((a.tokens + kWaves * 4 - 1) / (kWaves * 4)));
-    if (dtype == OPTIM_F32)
-        hipLaunchKernelGGL((route_kernel<V, D, OPTIM_F32>), grid, dim3(kThreads), 0, s, a, lay);
-    else if (dtype == OPTIM_BF16)
-        hipLaunchKernelGGL((route_kernel<V, D, OPTIM_BF16>), grid, dim3(kThreads), 0, s, a, lay);
-    else
-        hipLaunchKernelGGL((route_kernel<V, D, OPTIM_F16>), grid, dim3(kThreads), 0, s, a, lay);
+    lay.full = a.experts == 16 * V;
+    if (dtype == OPTIM_F32) return launch_route_t<V, D, OPTIM_F32>(a, lay, s);
+    if (dtype == OPTIM_BF16) return launch_route_t<V, D, OPTIM_BF16>(a, lay, s);
+    launch_route_t<V, D, OPTIM_F16>(a, lay, s);
 }
 template <int V>
 void launch_route_v(const RouteArgs &a, Lay lay, int dtype, hipStream_t s) {
@@ -649,19 +791,23 @@ void launch_route_v(const RouteArgs &a, Lay lay, int dtype, hipStream_t s) {
 // together.
 Lay lay_of(int32_t experts, int32_t groups) {
     const int32_t n = (experts + 15) / 16;
-    const Lay lay{groups > 1 ? n : (n + 3) / 4 * 4, false};
-    return Lay{lay.n, lay.n % 4 == 0 && experts % 4 == 0};
+    const int32_t each = groups > 1 ? n : (n + 3) / 4 * 4;
+    return Lay{each, each % 4 == 0 && experts % 4 == 0, false};
 }
-template <int V>
-hipError_t launch_route_grad_v(const RouteGradArgs &a, int dtype, hipStream_t s) {
-    const dim3 grid(route_grid(a.tokens));
-    if (dtype == OPTIM_F32)
-        hipLaunchKernelGGL((route_grad_kernel<V, OPTIM_F32>), grid, dim3(kThreads), 0, s, a);
-    else if (dtype == OPTIM_BF16)
-        hipLaunchKernelGGL((route_grad_kernel<V, OPTIM_BF16>), grid, dim3(kThreads), 0, s, a);
+template <int L, int C, int DT>
+void launch_route_grad_t(const RouteGradArgs &a, hipStream_t s) {
+    constexpr int64_t kTokens = kWaves * 64 / L;
+    const dim3 grid((unsigned)((a.tokens + kTokens - 1) / kTokens));
+    if (a.score == OPTIM_ROUTE_SOFTMAX && !a.renormalise)
+        hipLaunchKernelGGL((route_grad_kernel<L, C, DT, true>), grid, dim3(kThreads), 0, s, a);
     else
-        hipLaunchKernelGGL((route_grad_kernel<V, OPTIM_F16>), grid, dim3(kThreads), 0, s, a);
-    return hipGetLastError();
+        hipLaunchKernelGGL((route_grad_kernel<L, C, DT, false>), grid, dim3(kThreads), 0, s, a);
+}
+template <int L, int C>
+void launch_route_grad_c(const RouteGradArgs &a, int dtype, hipStream_t s) {
+    if (dtype == OPTIM_F32) return launch_route_grad_t<L, C, OPTIM_F32>(a, s);
+    if (dtype == OPTIM_BF16) return launch_route_grad_t<L, C, OPTIM_BF16>(a, s);
+    launch_route_grad_t<L, C, OPTIM_F16>(a, s);
 }
 
 }  // namespace
@@ -686,12 +832,15 @@ hipError_t launch_route(const RouteArgs &args, int dtype, hipStream_t s) {
     });
 }
 
-hipError_t launch_route_grad(const RouteGradArgs &a, int dtype, hipStream_t s) {
-    if (a.experts <= 64) return launch_route_grad_v<1>(a, dtype, s);
-    if (a.experts <= 128) return launch_route_grad_v<2>(a, dtype, s);
-    if (a.experts <= 256) return launch_route_grad_v<4>(a, dtype, s);
-    if (a.experts <= 512) return launch_route_grad_v<8>(a, dtype, s);
-    return launch_route_grad_v<16>(a, dtype, s);
+hipError_t launch_route_grad(const RouteGradArgs &args, int dtype, hipStream_t s) {
+    return route_slices(args, [&](const RouteGradArgs &a) {
+        if (a.topk > 16)
+            return a.experts <= 512 ? launch_route_grad_c<64, 1>(a, dtype, s) : launch_route_grad_c<64, 2>(a, dtype, s);
+        if (a.experts <= 128) return launch_route_grad_c<16, 1>(a, dtype, s);
+        if (a.experts <= 256) return launch_route_grad_c<16, 2>(a, dtype, s);
+        if (a.experts <= 512) return launch_route_grad_c<16, 4>(a, dtype, s);
+        return launch_route_grad_c<16, 8>(a, dtype, s);
+    });
 }
 
 }  // namespace optim
