@@ -3,12 +3,15 @@
 // (optim_step_route_bias).
 //
 // A workgroup takes a chunk of the choices, each of its wavefronts a run of 64s.
-// Choices without an expert are sorted behind the others, as expert E.  Where
-// one workgroup takes all, one launch counts, scans and places; otherwise a
-// first launch counts each chunk, and every workgroup of the second sums what
-// lies before its chunk.  A choice's place among the equal ones of its
-// wavefront's 64 comes from ballots over the bits of the expert: no atomics on
-// anything whose order could show.
+// Choices without an expert are sorted behind the others, as expert E.  A choice's
+// rank among the equal ones of its 64 comes from ballots over the bits of the
+// expert, and the wavefront's count so far from LDS: no atomics on anything whose
+// order could show, and none that many lanes would meet in where one expert is
+// far more popular.  Where one workgroup takes all, one launch counts, scans and
+// places; otherwise a first launch counts each chunk, and every workgroup of the
+// second sums what lies before its chunk.
+//
+// Bound by latency: 6 MB and a dependent chain of loads in each launch.
 #include "device_common.h"
 #include "experts.h"
 
@@ -17,7 +20,9 @@
 namespace optim {
 namespace {
 
-constexpr int kRowLanes = 512, kRowWaves = kRowLanes / 64;
+constexpr int kRowLanes = 1024, kRowWaves = kRowLanes / 64;  // of a workgroup, at most
+constexpr int kHeld = 16;                                    // 64s of a run that stay in registers
+constexpr int kBatch = 10;                                   // rows of counts that a lane asks for at a time
 typedef int32_t __attribute__((ext_vector_type(4))) s32x4;
 
 // What the wavefront's lanes read from LDS they have read, and what they wrote is
@@ -32,30 +37,56 @@ __device__ __forceinline__ int32_t expert_of(const RowsArgs &a, int32_t i) {
     return e < (uint32_t)a.experts ? (int32_t)e : a.experts;
 }
 
-// A wavefront's run of the chunk [c0, c1).  (No sum here passes c1, which may lie
-// just below 2^31.)
+// A wavefront's run of this workgroup's chunk.  (No sum here passes the chunk's
+// end, which may lie just below 2^31.)
 struct Run {
-    int32_t begin, end;
+    int32_t begin, n;
 };
-__device__ __forceinline__ Run wave_run(int32_t c0, int32_t c1, int32_t run) {
-    const int32_t wave = threadIdx.x >> 6, n = c1 - c0, lo = wave * run, hi = lo + run;
-    return Run{c0 + (lo < n ? lo : n), c0 + (hi < n ? hi : n)};
+__device__ __forceinline__ Run wave_run(const RowsArgs &a) {
+    const int32_t c0 = (int32_t)blockIdx.x * a.chunk, n = a.n - c0 < a.chunk ? a.n - c0 : a.chunk;
+    const int32_t run = a.chunk / (int32_t)(blockDim.x >> 6), lo = (int32_t)(threadIdx.x >> 6) * run, hi = lo + run;
+    const int32_t begin = lo < n ? lo : n;
+    return Run{c0 + begin, (hi < n ? hi : n) - begin};
 }
 
-// cnt[wave][expert]: choices of each wavefront's run of the chunk.  The first
-// kHeld of a lane's experts stay in registers.
-constexpr int kHeld = 8;
-__device__ __forceinline__ void count_chunk(const RowsArgs &a, const Run &r, int32_t *cnt, int32_t (&held)[kHeld]) {
-    const int32_t E1 = a.experts + 1, lane = threadIdx.x & 63, n = r.end - r.begin;
-    int32_t *mine = cnt + (threadIdx.x >> 6) * E1;
+// Counts the 64 choices that the lanes hold, e each (in: there is one), into the
+// wavefront's next[]; returns how many equal ones of the run came before.
+__device__ __forceinline__ int32_t count_64(int32_t e, bool in, int32_t bits, int32_t *next) {
+    const int32_t lane = threadIdx.x & 63;
+    const uint64_t there = __ballot(in);
+    uint32_t lo = (uint32_t)there, hi = (uint32_t)(there >> 32);
+    for (int b = 0; b < bits; ++b) {
+        const int32_t bit = (int32_t)((uint32_t)e << (31 - b)) >> 31;  // 0 or all ones
+        const uint64_t set = __ballot(bit);
+        lo &= ~((uint32_t)set ^ (uint32_t)bit);
+        hi &= ~((uint32_t)(set >> 32) ^ (uint32_t)bit);
+    }
+    const uint64_t same = (uint64_t)hi << 32 | lo;
+    const int32_t rank = __popcll(same & ((1ull << lane) - 1)), before = next[e];
+    wave_sync();
+    if (in && rank == 0) next[e] = before + __popcll(same);
+    wave_sync();
+    return before + rank;
+}
+
+// The run's counts in next[].  Its first choices stay in held[], expert and rank
+// (of at most 2^15 choices a workgroup: 16 bits) in one number.
+__device__ __forceinline__ void count_run(const RowsArgs &a, const Run &r, int32_t bits, int32_t *cnt, uint32_t (&held)[kHeld]) {
+    const int32_t E1 = a.experts + 1, lane = threadIdx.x & 63;
+    int32_t *next = cnt + (threadIdx.x >> 6) * E1;
 #pragma unroll
-    for (int h = 0; h < kHeld; ++h) held[h] = h * 64 + lane < n ? expert_of(a, r.begin + h * 64 + lane) : a.experts;
-    for (int32_t i = threadIdx.x; i < kRowWaves * E1; i += kRowLanes) cnt[i] = 0;
+    for (int h = 0; h < kHeld; ++h) held[h] = h * 64 + lane < r.n ? (uint32_t)expert_of(a, r.begin + h * 64 + lane) : 0u;
+    for (int32_t i = threadIdx.x; i < (int32_t)(blockDim.x >> 6) * E1; i += blockDim.x) cnt[i] = 0;
     __syncthreads();
 #pragma unroll
-    for (int h = 0; h < kHeld; ++h)
-        if (h * 64 + lane < n) atomicAdd(&mine[held[h]], 1);
-    for (int32_t i = kHeld * 64 + lane; i < n; i += 64) atomicAdd(&mine[expert_of(a, r.begin + i)], 1);
+    for (int h = 0; h < kHeld; ++h) {
+        if (h * 64 >= r.n) break;
+        held[h] |= (uint32_t)count_64((int32_t)held[h], h * 64 + lane < r.n, bits, next) << 16;
+    }
+    for (int32_t i0 = kHeld * 64; i0 < r.n; i0 += 64) {
+        const bool in = i0 + lane < r.n;
+        count_64(in ? expert_of(a, r.begin + i0 + lane) : 0, in, bits, next);
+    }
     __syncthreads();
 }
 
@@ -64,79 +95,70 @@ __device__ __forceinline__ int32_t count_row(const RowsArgs &a) { return (a.expe
 
 __global__ __launch_bounds__(kRowLanes) void rows_count_kernel(RowsArgs a) {
     __shared__ int32_t cnt[kRowWaves * (kMaxExperts + 1)];
-    const int32_t E1 = a.experts + 1, c0 = (int32_t)blockIdx.x * a.chunk;
-    const int32_t c1 = a.n - c0 < a.chunk ? a.n : c0 + a.chunk;
-    int32_t held[kHeld];
-    count_chunk(a, wave_run(c0, c1, a.chunk / kRowWaves), cnt, held);
-    for (int32_t e = threadIdx.x; e < E1; e += kRowLanes) {
+    const int32_t E1 = a.experts + 1, bits = 32 - __builtin_clz(a.experts);
+    uint32_t held[kHeld];
+    count_run(a, wave_run(a), bits, cnt, held);
+    for (int32_t e = threadIdx.x; e < E1; e += blockDim.x) {
         int32_t sum = 0;
-        for (int w = 0; w < kRowWaves; ++w) sum += cnt[w * E1 + e];
+        for (uint32_t w = 0; w < blockDim.x >> 6; ++w) sum += cnt[w * E1 + e];
         a.counts[(int64_t)blockIdx.x * count_row(a) + e] = sum;
     }
 }
 
-// The 64 choices that a wavefront's lanes hold, e each (in: there is one): rows
-// in the order of lanes, from next[] on, which moves on.
-__device__ __forceinline__ void place_64(const RowsArgs &a, int32_t i, int32_t e, bool in, int32_t bits, int32_t *next) {
-    const int32_t lane = threadIdx.x & 63;
-    uint64_t same = __ballot(in);
-    for (int b = 0; b < bits; ++b) {
-        const uint64_t set = __ballot(e >> b & 1);
-        same &= e >> b & 1 ? set : ~set;
-    }
-    const int32_t rank = __popcll(same & ((1ull << lane) - 1));
-    const int32_t row = in ? next[e] + rank : 0;
-    wave_sync();
-    if (in && rank == 0) next[e] += __popcll(same);
-    wave_sync();
-    if (in) {
-        a.place[i] = e < a.experts ? row : -1;
-        if (a.order) a.order[row] = e < a.experts ? i : -1;
-    }
+__device__ __forceinline__ void put_row(const RowsArgs &a, int32_t i, int32_t e, int32_t row) {
+    a.place[i] = e < a.experts ? row : -1;
+    if (a.order) a.order[row] = e < a.experts ? i : -1;
 }
 
 __global__ __launch_bounds__(kRowLanes) void rows_place_kernel(RowsArgs a) {
     __shared__ int32_t cnt[kRowWaves * (kMaxExperts + 1)];
     __shared__ int32_t all[kMaxExperts + 4], before[kMaxExperts + 4];
-    const int32_t E1 = a.experts + 1, c0 = (int32_t)blockIdx.x * a.chunk;
-    const int32_t c1 = a.n - c0 < a.chunk ? a.n : c0 + a.chunk;
+    const int32_t E1 = a.experts + 1, bits = 32 - __builtin_clz(a.experts), waves = blockDim.x >> 6;
     const int32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const Run r = wave_run(c0, c1, a.chunk / kRowWaves);
-    int32_t held[kHeld];
-    for (int32_t e = threadIdx.x; e < count_row(a); e += kRowLanes) {
+    const Run r = wave_run(a);
+    // Lanes take four experts' counts in every slices-th chunk, kBatch loads at a
+    // time, the first ones before anything else.
+    const int32_t quads = count_row(a) / 4, slices = (int32_t)blockDim.x / quads, slice = threadIdx.x / quads;
+    const int32_t q = threadIdx.x % quads;
+    const bool sums = a.counts && slice < slices;
+    s32x4 v[kBatch];
+    auto load = [&](int32_t b0) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int32_t b = b0 + i * slices;
+            v[i] = *(const GMEM s32x4 *)gp(a.counts + ((int64_t)(b < a.blocks ? b : slice) * quads + q) * 4);
+        }
+    };
+    if (sums && slice < a.blocks) load(slice);
+    for (int32_t e = threadIdx.x; e < count_row(a); e += blockDim.x) {
         all[e] = 0;
         before[e] = 0;
     }
-    count_chunk(a, r, cnt, held);
-    if (a.counts) {
-        // Lanes take four experts and every slices-th chunk, eight loads at a time.
-        const int32_t quads = count_row(a) / 4, slices = kRowLanes / quads, slice = threadIdx.x / quads, q = threadIdx.x % quads;
-        if (slice < slices) {
-            s32x4 sum = {0, 0, 0, 0}, low = {0, 0, 0, 0};
-            for (int32_t b0 = slice; b0 < a.blocks; b0 += 8 * slices) {
-                s32x4 v[8];
+    uint32_t held[kHeld];
+    count_run(a, r, bits, cnt, held);
+    if (sums) {
+        s32x4 sum = {0, 0, 0, 0}, low = {0, 0, 0, 0};
+        for (int32_t b0 = slice; b0 < a.blocks; b0 += kBatch * slices) {
+            if (b0 > slice) load(b0);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int32_t b = b0 + i * slices;
-                    v[i] = *(const GMEM s32x4 *)gp(a.counts + ((int64_t)(b < a.blocks ? b : b0) * quads + q) * 4);
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int32_t b = b0 + i * slices;
-                    if (b < a.blocks) sum += v[i];
-                    if (b < (int32_t)blockIdx.x) low += v[i];
-                }
+            for (int i = 0; i < kBatch; ++i) {
+                const int32_t b = b0 + i * slices;
+                if (b < a.blocks) sum += v[i];
+                if (b < (int32_t)blockIdx.x) low += v[i];
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (q * 4 + i < E1) {
-                    atomicAdd(&all[q * 4 + i], sum[i]);
-                    atomicAdd(&before[q * 4 + i], low[i]);
-                }
         }
-    } else {
-        for (int32_t e = threadIdx.x; e < E1; e += kRowLanes)
-            for (int w = 0; w < kRowWaves; ++w) all[e] += cnt[w * E1 + e];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (q * 4 + i < E1) {
+                atomicAdd(&all[q * 4 + i], sum[i]);
+                atomicAdd(&before[q * 4 + i], low[i]);
+            }
+    } else if (!a.counts) {
+        for (int32_t e = threadIdx.x; e < E1; e += blockDim.x) {
+            int32_t sum = 0;
+            for (int w = 0; w < waves; ++w) sum += cnt[w * E1 + e];
+            all[e] = sum;
+        }
     }
     __syncthreads();
     if (wave == 0) {  // all: number of choices -> first row
@@ -145,39 +167,41 @@ __global__ __launch_bounds__(kRowLanes) void rows_place_kernel(RowsArgs a) {
         for (int32_t i = e0; i < e0 + per && i < E1; ++i) sum += all[i];
         int32_t first = sum;
         for (int m = 1; m < 64; m *= 2) {
-            const int32_t v = __shfl_up(first, m);
-            if (lane >= m) first += v;
+            const int32_t up = __shfl_up(first, m);
+            if (lane >= m) first += up;
         }
         first -= sum;
         for (int32_t i = e0; i < e0 + per && i < E1; ++i) {
-            const int32_t v = all[i];
+            const int32_t c = all[i];
             all[i] = first;
-            first += v;
+            first += c;
         }
     }
     __syncthreads();
-    for (int32_t e = threadIdx.x; e < E1; e += kRowLanes) {
+    for (int32_t e = threadIdx.x; e < E1; e += blockDim.x) {
         if (blockIdx.x == 0) a.offsets[e] = all[e];
         int32_t at = all[e] + before[e];
-        for (int w = 0; w < kRowWaves; ++w) {
-            const int32_t v = cnt[w * E1 + e];
+        for (int w = 0; w < waves; ++w) {  // cnt: number of choices -> the run's first row
+            const int32_t c = cnt[w * E1 + e];
             cnt[w * E1 + e] = at;
-            at += v;
+            at += c;
         }
     }
     __syncthreads();
-    const int32_t bits = 32 - __builtin_clz(a.experts), n = r.end - r.begin;
     int32_t *next = cnt + wave * E1;
+    if (a.chunk <= kHeld * (int32_t)blockDim.x) {  // all choices are held
 #pragma unroll
-    for (int h = 0; h < kHeld; ++h) {
-        if (h * 64 >= n) break;
-        const bool in = h * 64 + lane < n;
-        place_64(a, r.begin + (in ? h * 64 + lane : 0), held[h], in, bits, next);
+        for (int h = 0; h < kHeld; ++h)
+            if (h * 64 + lane < r.n) {
+                const int32_t e = held[h] & 0xFFFF;
+                put_row(a, r.begin + h * 64 + lane, e, next[e] + (int32_t)(held[h] >> 16));
+            }
+        return;
     }
-    for (int32_t i0 = kHeld * 64; i0 < n; i0 += 64) {
-        const bool in = i0 + lane < n;
-        const int32_t i = r.begin + (in ? i0 + lane : 0);
-        place_64(a, i, in ? expert_of(a, i) : 0, in, bits, next);
+    for (int32_t i0 = 0; i0 < r.n; i0 += 64) {
+        const bool in = i0 + lane < r.n;
+        const int32_t e = in ? expert_of(a, r.begin + i0 + lane) : 0, row = count_64(e, in, bits, next);
+        if (in) put_row(a, r.begin + i0 + lane, e, row);
     }
 }
 
@@ -194,10 +218,11 @@ __global__ __launch_bounds__(kMaxExperts) void route_bias_kernel(const int32_t *
 
 }  // namespace
 
+// One workgroup up to 8192 choices, then 128 of them (each of which reads the
+// counts of all), more once each has kHeld 64s a wavefront, and 512 at most.
 RowsShape rows_shape(int64_t n) {
-    // 128 workgroups of the second launch sum as many counts each; more of them
-    // once each has 16384 choices, 512 at most.
-    int64_t chunk = std::max<int64_t>({n / 512, std::min<int64_t>(n / 128, 16384), 4096});
+    constexpr int64_t kAll = kHeld * kRowLanes;
+    int64_t chunk = n <= 8192 ? 8192 : std::max<int64_t>({n / 512, std::min<int64_t>(n / 128, kAll), 4096});
     chunk += kRowLanes - 1;
     chunk -= chunk % kRowLanes;
     return RowsShape{(int32_t)chunk, (int32_t)((n + chunk - 1) / chunk)};
@@ -207,9 +232,15 @@ size_t rows_workspace(RowsShape shape, int32_t experts) {
     return shape.blocks > 1 ? (size_t)shape.blocks * ((experts + 4) / 4 * 4) * sizeof(int32_t) : 0;
 }
 
-hipError_t launch_rows(const RowsArgs &a, hipStream_t s) {
-    if (a.counts) hipLaunchKernelGGL(rows_count_kernel, dim3((unsigned)a.blocks), dim3(kRowLanes), 0, s, a);
-    hipLaunchKernelGGL(rows_place_kernel, dim3((unsigned)(a.blocks > 0 ? a.blocks : 1)), dim3(kRowLanes), 0, s, a);
+hipError_t launch_rows(const RowsArgs &args, hipStream_t s) {
+    RowsArgs a = args;
+    dim3 lanes(kRowLanes);
+    if (!a.counts && a.n <= 1024) {  // fewer wavefronts to wait for
+        a.chunk = 1024;
+        lanes = dim3(256);
+    }
+    if (a.counts) hipLaunchKernelGGL(rows_count_kernel, dim3((unsigned)a.blocks), lanes, 0, s, a);
+    hipLaunchKernelGGL(rows_place_kernel, dim3((unsigned)(a.blocks > 0 ? a.blocks : 1)), lanes, 0, s, a);
     return hipGetLastError();
 }
 

@@ -42,7 +42,7 @@ def test_small(tokens, topk, experts, nowhere):
         assert np.array_equal(got.cpu().numpy(), w)
 
 
-@pytest.mark.parametrize("tokens,topk,experts", [(4100, 1, 3), (65536, 8, 256), (70001, 7, 512), (30011, 6, 1000), (600001, 4, 16), (3000000, 2, 2)])
+@pytest.mark.parametrize("tokens,topk,experts", [(4100, 1, 3), (65536, 8, 256), (70001, 7, 512), (30011, 6, 1000), (600001, 4, 16), (3000000, 2, 2), (6000001, 2, 300)])
 @pytest.mark.parametrize("nowhere", [0.0, 0.1])
 def test_large(tokens, topk, experts, nowhere):
     idx = choices(tokens, tokens, topk, experts, nowhere, 3.0)
