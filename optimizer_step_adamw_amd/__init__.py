@@ -218,10 +218,27 @@ def _ptr(t) -> Optional[int]:
 
 
 def _stream(stream) -> Optional[int]:
-    import torch
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return _current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+_current = None
+
+
+def _current_stream() -> int:
+    """Handle of the current device's current stream: torch's own short way to
+    it, where this torch has it, takes a tenth of torch.cuda.current_stream()'s
+    time."""
+    global _current
+    if _current is None:
+        import torch
+        raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+        if raw is None or device is None:
+            return torch.cuda.current_stream().cuda_stream
+        torch.cuda.current_stream()  # (brings the runtime up)
+        _current = lambda: raw(device())  # noqa: E731
+    return _current()
 
 
 # --------------------------------------------------------------------------
@@ -456,31 +473,59 @@ def optim_expert_grad(x, dy, offsets, dw, *, accumulate: bool = False, scale=Non
 
 # --------------------------------------------------------------------------
 # routing, the experts' rows, dropout (optim_route.h, optim_dropout.h)
+# (These calls may take less time on the GPU than their arguments' checks on the
+# host, so the checks ask each tensor for as little as they can.)
+_torch = None
+_float_codes: dict = {}
+
+
+def _types():
+    global _torch
+    if _torch is None:
+        import torch
+        _float_codes.update({torch.float32: OPTIM_F32, torch.bfloat16: OPTIM_BF16, torch.float16: OPTIM_F16})
+        _torch = torch
+    return _torch
+
+
 def _float_code(*tensors) -> int:
     """The one dtype code of the tensors that are given."""
-    import torch
-    codes = {torch.float32: OPTIM_F32, torch.bfloat16: OPTIM_BF16, torch.float16: OPTIM_F16}
-    kinds = {t.dtype for t in tensors if t is not None}
-    if len(kinds) != 1 or not kinds <= set(codes):
-        raise ValueError(f"expected tensors of one type, float32, bfloat16 or float16, got {sorted(map(str, kinds))}")
-    return codes[kinds.pop()]
+    _types()
+    dtype = None
+    for t in tensors:
+        if t is not None and t.dtype is not dtype:
+            if dtype is not None or t.dtype not in _float_codes:
+                raise ValueError("expected tensors of one type, float32, bfloat16 or float16, got "
+                                 f"{[str(x.dtype) for x in tensors if x is not None]}")
+            dtype = t.dtype
+    return _float_codes[dtype]
 
 
-def _expect(t, dtype: str, shape, what: str):
-    """Address of a contiguous tensor of that type and shape; None passes through."""
+def _expect(t, dtype, shape, what: str):
+    """Address of a contiguous GPU tensor of that type and shape; None passes through."""
     if t is None:
         return None
-    if str(t.dtype) != "torch." + dtype or tuple(t.shape) != tuple(shape):
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{what}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    return _ptr(t)
+    if not t.is_cuda or not t.is_contiguous():
+        return _ptr(t)  # says what is wrong
+    return t.data_ptr()
 
 
-def _scalar(t, dtype: str, what: str):
+def _one(t, dtype, what: str):
     if t is None:
         return None
-    if str(t.dtype) != "torch." + dtype or t.numel() != 1:
+    if t.dtype is not dtype or t.numel() != 1:
         raise ValueError(f"{what}: expected one {dtype}, got {t.dtype} {tuple(t.shape)}")
-    return _ptr(t)
+    return t.data_ptr() if t.is_cuda else _ptr(t)
+
+
+def _matrix(t, what: str):
+    """Address and row distance of a matrix, for one whose rows lie end to end
+    without asking for its strides."""
+    if t.is_cuda and t.dim() == 2 and t.is_contiguous():
+        return t.data_ptr(), t.shape[1]
+    return _rows(t, what)
 
 
 def _by_ref(hp):
@@ -491,31 +536,32 @@ def optim_route(logits, hp: optim_route_hp, idx, weights, *, bias=None, stream=N
     """logits [tokens, experts] (rows may lie apart), idx int32 and weights
     float32 [tokens, topk], bias float32 [experts]."""
     code = _float_code(logits)
-    p, ld = _rows(logits, "logits")
+    p, ld = _matrix(logits, "logits")
     t, e = logits.shape
-    _check(lib().optim_route(p, ld, code, t, e, _expect(bias, "float32", (e,), "bias"), ctypes.byref(hp),
-                             _expect(idx, "int32", (t, hp.topk), "idx"),
-                             _expect(weights, "float32", (t, hp.topk), "weights"), _stream(stream)), "optim_route")
+    _check(lib().optim_route(p, ld, code, t, e, _expect(bias, _torch.float32, (e,), "bias"), ctypes.byref(hp),
+                             _expect(idx, _torch.int32, (t, hp.topk), "idx"),
+                             _expect(weights, _torch.float32, (t, hp.topk), "weights"), _stream(stream)), "optim_route")
 
 
 def optim_route_grad(logits, hp: optim_route_hp, idx, dweights, dlogits, *, stream=None) -> None:
     """dlogits: type and shape of logits (rows of both may lie apart)."""
     code = _float_code(logits, dlogits)
-    (p, ld), (pd, ldd) = _rows(logits, "logits"), _rows(dlogits, "dlogits")
+    (p, ld), (pd, ldd) = _matrix(logits, "logits"), _matrix(dlogits, "dlogits")
     if logits.shape != dlogits.shape:
         raise ValueError(f"shapes do not fit: logits {tuple(logits.shape)}, dlogits {tuple(dlogits.shape)}")
     t, e = logits.shape
-    _check(lib().optim_route_grad(p, ld, code, t, e, ctypes.byref(hp), _expect(idx, "int32", (t, hp.topk), "idx"),
-                                  _expect(dweights, "float32", (t, hp.topk), "dweights"), pd, ldd, _stream(stream)),
+    _check(lib().optim_route_grad(p, ld, code, t, e, ctypes.byref(hp), _expect(idx, _torch.int32, (t, hp.topk), "idx"),
+                                  _expect(dweights, _torch.float32, (t, hp.topk), "dweights"), pd, ldd, _stream(stream)),
            "optim_route_grad")
 
 
 def optim_step_route_bias(offsets, bias, rate, *, found_inf=None, stream=None) -> None:
     """offsets int32 [experts + 1], bias float32 [experts], rate one float32."""
+    _types()
     e = bias.numel()
-    _check(lib().optim_step_route_bias(_expect(offsets, "int32", (e + 1,), "offsets"), e,
-                                       _expect(bias, "float32", (e,), "bias"), _scalar(rate, "float32", "rate"),
-                                       _scalar(found_inf, "float32", "found_inf"), _stream(stream)),
+    _check(lib().optim_step_route_bias(_expect(offsets, _torch.int32, (e + 1,), "offsets"), e,
+                                       _expect(bias, _torch.float32, (e,), "bias"), _one(rate, _torch.float32, "rate"),
+                                       _one(found_inf, _torch.float32, "found_inf"), _stream(stream)),
            "optim_step_route_bias")
 
 
@@ -530,34 +576,36 @@ def optim_route_rows(idx, offsets, place, *, order=None, workspace=None, stream=
     """idx and place int32 [tokens, topk], offsets int32 [experts + 1], order
     int32 [tokens * topk], workspace: a tensor of at least
     optim_route_rows_workspace bytes."""
+    _types()
     if idx.dim() != 2 or offsets.dim() != 1:
         raise ValueError(f"shapes do not fit: idx {tuple(idx.shape)}, offsets {tuple(offsets.shape)}")
     t, k = idx.shape
     nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _check(lib().optim_route_rows(_expect(idx, "int32", (t, k), "idx"), t, k, offsets.numel() - 1,
-                                  _expect(offsets, "int32", (offsets.numel(),), "offsets"),
-                                  _expect(place, "int32", (t, k), "place"), _expect(order, "int32", (t * k,), "order"),
+    _check(lib().optim_route_rows(_expect(idx, _torch.int32, (t, k), "idx"), t, k, offsets.numel() - 1,
+                                  _expect(offsets, _torch.int32, (offsets.numel(),), "offsets"),
+                                  _expect(place, _torch.int32, (t, k), "place"), _expect(order, _torch.int32, (t * k,), "order"),
                                   _ptr(workspace), nbytes, _stream(stream)), "optim_route_rows")
 
 
-def _token_shapes(by_token, by_row, place):
+def _token_shapes(place, by_token, by_row):
     """(tokens, topk, dim, rows) of matrices by token and by row."""
-    sizes = [m.shape for m in (*by_token, *by_row) if m is not None]
-    if place.dim() != 2 or any(len(s) != 2 or s[1] != sizes[0][1] for s in sizes) or any(
-            m.shape[0] != place.shape[0] for m in by_token if m is not None) or len(
-            {m.shape[0] for m in by_row if m is not None}) != 1:
-        raise ValueError(f"shapes do not fit: {[tuple(s) for s in sizes]}, place {tuple(place.shape)}")
-    return place.shape[0], place.shape[1], sizes[0][1], [m for m in by_row if m is not None][0].shape[0]
+    t, k = place.shape if place.dim() == 2 else (-1, 0)
+    by_token, by_row = [m.shape for m in by_token if m is not None], [m.shape for m in by_row if m is not None]
+    dim, rows = (by_token[0] or (0,))[-1], (by_row[0] or (0,))[0]
+    if any(s != (t, dim) for s in by_token) or any(s != (rows, dim) for s in by_row):
+        raise ValueError(f"shapes do not fit: by token {[tuple(s) for s in by_token]}, by row {[tuple(s) for s in by_row]}, "
+                         f"place {tuple(place.shape)}")
+    return t, k, dim, rows
 
 
 def optim_expert_gather(x, place, y, *, weights=None, stream=None) -> None:
     """x [tokens, dim], y [rows, dim] of one type (rows may lie apart), place
     int32 and weights float32 [tokens, topk]."""
     code = _float_code(x, y)
-    t, k, dim, rows = _token_shapes((x,), (y,), place)
-    (px, ldx), (py, ldy) = _rows(x, "x"), _rows(y, "y")
-    _check(lib().optim_expert_gather(px, ldx, code, _expect(place, "int32", (t, k), "place"),
-                                     _expect(weights, "float32", (t, k), "weights"), t, k, dim, py, ldy, rows,
+    t, k, dim, rows = _token_shapes(place, (x,), (y,))
+    (px, ldx), (py, ldy) = _matrix(x, "x"), _matrix(y, "y")
+    _check(lib().optim_expert_gather(px, ldx, code, _expect(place, _torch.int32, (t, k), "place"),
+                                     _expect(weights, _torch.float32, (t, k), "weights"), t, k, dim, py, ldy, rows,
                                      _stream(stream)), "optim_expert_gather")
 
 
@@ -567,12 +615,12 @@ def optim_expert_combine(y, place, out, *, weights=None, residual=None, dropout:
     apart; out may be residual), place int32 and weights float32 [tokens, topk],
     step one int32."""
     code = _float_code(y, out, residual)
-    t, k, dim, rows = _token_shapes((out, residual), (y,), place)
-    (py, ldy), (po, ldo) = _rows(y, "y"), _rows(out, "out")
-    pr, ldr = _rows(residual, "residual") if residual is not None else (None, 0)
-    _check(lib().optim_expert_combine(py, ldy, rows, code, _expect(place, "int32", (t, k), "place"),
-                                      _expect(weights, "float32", (t, k), "weights"), t, k, dim, pr, ldr, _by_ref(dropout),
-                                      _scalar(step, "int32", "step"), po, ldo, _stream(stream)), "optim_expert_combine")
+    t, k, dim, rows = _token_shapes(place, (out, residual), (y,))
+    (py, ldy), (po, ldo) = _matrix(y, "y"), _matrix(out, "out")
+    pr, ldr = _matrix(residual, "residual") if residual is not None else (None, 0)
+    _check(lib().optim_expert_combine(py, ldy, rows, code, _expect(place, _torch.int32, (t, k), "place"),
+                                      _expect(weights, _torch.float32, (t, k), "weights"), t, k, dim, pr, ldr, _by_ref(dropout),
+                                      _one(step, _torch.int32, "step"), po, ldo, _stream(stream)), "optim_expert_combine")
 
 
 def optim_expert_combine_grad(dout, y, place, dy, *, weights=None, dweights=None, dropout: Optional[optim_dropout_hp] = None,
@@ -583,14 +631,14 @@ def optim_expert_combine_grad(dout, y, place, dy, *, weights=None, dweights=None
     code = _float_code(dout, y, dy)
     if y is None and (dy is None or dweights is not None):
         raise ValueError("dweights takes y, and without it there must be dy")
-    t, k, dim, rows = _token_shapes((dout,), (y, dy), place)
-    pd, ldd = _rows(dout, "dout")
-    py, ldy = _rows(y, "y") if y is not None else (None, 0)
-    pg, ldg = _rows(dy, "dy") if dy is not None else (None, 0)
-    _check(lib().optim_expert_combine_grad(pd, ldd, code, py, ldy, rows, _expect(place, "int32", (t, k), "place"),
-                                           _expect(weights, "float32", (t, k), "weights"), t, k, dim, _by_ref(dropout),
-                                           _scalar(step, "int32", "step"), pg, ldg,
-                                           _expect(dweights, "float32", (t, k), "dweights"), _stream(stream)),
+    t, k, dim, rows = _token_shapes(place, (dout,), (y, dy))
+    pd, ldd = _matrix(dout, "dout")
+    py, ldy = _matrix(y, "y") if y is not None else (None, 0)
+    pg, ldg = _matrix(dy, "dy") if dy is not None else (None, 0)
+    _check(lib().optim_expert_combine_grad(pd, ldd, code, py, ldy, rows, _expect(place, _torch.int32, (t, k), "place"),
+                                           _expect(weights, _torch.float32, (t, k), "weights"), t, k, dim, _by_ref(dropout),
+                                           _one(step, _torch.int32, "step"), pg, ldg,
+                                           _expect(dweights, _torch.float32, (t, k), "dweights"), _stream(stream)),
            "optim_expert_combine_grad")
 
 
@@ -601,7 +649,7 @@ def optim_dropout(x, out, hp: optim_dropout_hp, *, residual=None, step=None, str
     if out.numel() != x.numel() or (residual is not None and residual.numel() != x.numel()):
         raise ValueError(f"sizes do not fit: x {tuple(x.shape)}, out {tuple(out.shape)}, residual "
                          f"{None if residual is None else tuple(residual.shape)}")
-    _check(lib().optim_dropout(_ptr(x), code, x.numel(), _ptr(residual), ctypes.byref(hp), _scalar(step, "int32", "step"),
+    _check(lib().optim_dropout(_ptr(x), code, x.numel(), _ptr(residual), ctypes.byref(hp), _one(step, _torch.int32, "step"),
                                _ptr(out), _stream(stream)), "optim_dropout")
 
 
