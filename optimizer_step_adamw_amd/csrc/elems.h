@@ -22,24 +22,50 @@ struct Raw8 {
     u32x4 v[DT == OPTIM_F32 ? 2 : 1];
 };
 
-template <int DT>
+// NT: past the caches, for what is larger than they are.  DT: whose alignment the
+// address has.
+template <int DT, bool NT>
+__device__ __forceinline__ u32x4 load_v(const char *p) {
+    if constexpr (DT == OPTIM_F32) {
+        const GMEM u32x4_at4 *q = (const GMEM u32x4_at4 *)gp(p);
+        if constexpr (NT) return __builtin_nontemporal_load(q);
+        else return *q;
+    } else {
+        const GMEM u32x4_at2 *q = (const GMEM u32x4_at2 *)gp(p);
+        if constexpr (NT) return __builtin_nontemporal_load(q);
+        else return *q;
+    }
+}
+template <int DT, bool NT>
+__device__ __forceinline__ void store_v(char *p, u32x4 x) {
+    if constexpr (DT == OPTIM_F32) {
+        GMEM u32x4_at4 *q = (GMEM u32x4_at4 *)gp(p);
+        if constexpr (NT) __builtin_nontemporal_store(x, q);
+        else *q = x;
+    } else {
+        GMEM u32x4_at2 *q = (GMEM u32x4_at2 *)gp(p);
+        if constexpr (NT) __builtin_nontemporal_store(x, q);
+        else *q = x;
+    }
+}
+template <int DT, bool NT = false>
 __device__ __forceinline__ Raw8<DT> load8(const char *p) {
     Raw8<DT> r;
     if constexpr (DT == OPTIM_F32) {
-        r.v[0] = *(const GMEM u32x4_at4 *)gp(p);
-        r.v[1] = *(const GMEM u32x4_at4 *)gp(p + 16);
+        r.v[0] = load_v<DT, NT>(p);
+        r.v[1] = load_v<DT, NT>(p + 16);
     } else {
-        r.v[0] = *(const GMEM u32x4_at2 *)gp(p);
+        r.v[0] = load_v<DT, NT>(p);
     }
     return r;
 }
-template <int DT>
+template <int DT, bool NT = false>
 __device__ __forceinline__ void store8(char *p, const Raw8<DT> &r) {
     if constexpr (DT == OPTIM_F32) {
-        *(GMEM u32x4_at4 *)gp(p) = r.v[0];
-        *(GMEM u32x4_at4 *)gp(p + 16) = r.v[1];
+        store_v<DT, NT>(p, r.v[0]);
+        store_v<DT, NT>(p + 16, r.v[1]);
     } else {
-        *(GMEM u32x4_at2 *)gp(p) = r.v[0];
+        store_v<DT, NT>(p, r.v[0]);
     }
 }
 
@@ -65,11 +91,11 @@ __device__ __forceinline__ void store_some(char *p, int n, const Raw8<DT> &r) {
     }
 }
 // n: elements from p on that exist.
-template <int DT>
-__device__ __forceinline__ Raw8<DT> get8(const char *p, int n) { return n >= 8 ? load8<DT>(p) : load_some<DT>(p, n); }
-template <int DT>
+template <int DT, bool NT = false>
+__device__ __forceinline__ Raw8<DT> get8(const char *p, int n) { return n >= 8 ? load8<DT, NT>(p) : load_some<DT>(p, n); }
+template <int DT, bool NT = false>
 __device__ __forceinline__ void put8(char *p, int n, const Raw8<DT> &r) {
-    if (n >= 8) store8<DT>(p, r);
+    if (n >= 8) store8<DT, NT>(p, r);
     else store_some<DT>(p, n, r);
 }
 

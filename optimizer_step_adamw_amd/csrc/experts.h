@@ -10,6 +10,9 @@
 
 namespace optim {
 
+// Bytes of a call from which on its large arrays pass by the caches.
+constexpr int64_t kPastCaches = int64_t(256) << 20;
+
 constexpr int32_t kMaxExperts = 1024, kMaxTopk = 32, kMaxExpertGroups = 64;
 
 struct RouteArgs {

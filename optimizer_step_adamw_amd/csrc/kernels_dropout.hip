@@ -8,7 +8,7 @@
 namespace optim {
 namespace {
 
-template <int DT, bool RES>
+template <int DT, bool RES, bool NT>
 __global__ __launch_bounds__(kThreads) void dropout_kernel(const char *x, const char *res, char *out, int64_t n, DropArgs d) {
     const uint32_t step = drop_step(d);
     const int64_t lead = d.first & 7;  // places of the first block that lie before element 0
@@ -18,14 +18,14 @@ __global__ __launch_bounds__(kThreads) void dropout_kernel(const char *x, const 
         const Words w = philox((uint64_t)((d.first >> 3) + b), step, d.site, d.seed);
         if (e >= 0 && e + 8 <= n) {
             float v[8], r[8];
-            floats<DT>(load8<DT>(x + e * kElem<DT>), v);
-            if constexpr (RES) floats<DT>(load8<DT>(res + e * kElem<DT>), r);
+            floats<DT>(load8<DT, NT>(x + e * kElem<DT>), v);
+            if constexpr (RES) floats<DT>(load8<DT, NT>(res + e * kElem<DT>), r);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 v[i] = draw_of(w, i) < d.bar ? 0.0f : v[i] * d.scale;
                 if constexpr (RES) v[i] = r[i] + v[i];
             }
-            store8<DT>(out + e * kElem<DT>, rounded<DT>(v));
+            store8<DT, NT>(out + e * kElem<DT>, rounded<DT>(v));
             continue;
         }
 #pragma unroll
@@ -38,16 +38,20 @@ __global__ __launch_bounds__(kThreads) void dropout_kernel(const char *x, const 
     }
 }
 
-template <int DT>
-hipError_t launch_dropout_t(const char *x, const char *residual, char *out, int64_t n, const DropArgs &d, hipStream_t s) {
+template <int DT, bool RES>
+hipError_t launch_dropout_r(const char *x, const char *residual, char *out, int64_t n, const DropArgs &d, hipStream_t s) {
     const int64_t blocks = (n + 14) / 8;
     const int64_t g = (blocks + kThreads - 1) / kThreads;
     const dim3 grid((unsigned)(g < (1 << 23) ? g : 1 << 23));
-    if (residual)
-        hipLaunchKernelGGL((dropout_kernel<DT, true>), grid, dim3(kThreads), 0, s, x, residual, out, n, d);
+    if (n * kElem<DT> * (RES ? 3 : 2) > kPastCaches)
+        hipLaunchKernelGGL((dropout_kernel<DT, RES, true>), grid, dim3(kThreads), 0, s, x, residual, out, n, d);
     else
-        hipLaunchKernelGGL((dropout_kernel<DT, false>), grid, dim3(kThreads), 0, s, x, residual, out, n, d);
+        hipLaunchKernelGGL((dropout_kernel<DT, RES, false>), grid, dim3(kThreads), 0, s, x, residual, out, n, d);
     return hipGetLastError();
+}
+template <int DT>
+hipError_t launch_dropout_t(const char *x, const char *residual, char *out, int64_t n, const DropArgs &d, hipStream_t s) {
+    return residual ? launch_dropout_r<DT, true>(x, residual, out, n, d, s) : launch_dropout_r<DT, false>(x, residual, out, n, d, s);
 }
 
 }  // namespace

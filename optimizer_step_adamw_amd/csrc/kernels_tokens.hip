@@ -52,7 +52,7 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(TokenArgs a, int lp) {
 // first one and counts for nothing, so that no load waits for another.
 constexpr int kAtOnce = 4;
 
-template <int DT, bool DROP>
+template <int DT, bool DROP, bool NT>
 __global__ __launch_bounds__(kThreads) void combine_kernel(TokenArgs a, int lp) {
     const Slot s = slot(lp);
     const int n = a.dim - s.c * 8;
@@ -61,7 +61,7 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(TokenArgs a, int lp) 
     const uint32_t step = DROP ? drop_step(a.drop) : 0u;
     for (int64_t t = s.t; t < a.tokens; t += s.dt) {
         Raw8<DT> res{};
-        if (a.x) res = get8<DT>(a.x + t * a.ldx + at, n);
+        if (a.x) res = get8<DT, NT>(a.x + t * a.ldx + at, n);
         float sum[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
         for (int32_t j0 = 0; j0 < a.topk && a.rows > 0; j0 += kAtOnce) {
             uint32_t r[kAtOnce];
@@ -74,7 +74,7 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(TokenArgs a, int lp) 
                 w[j] = a.weights ? a.weights[of] : 1.0f;
             }
 #pragma unroll
-            for (int j = 0; j < kAtOnce; ++j) y[j] = get8<DT>(a.y + (r[j] < a.rows ? r[j] : 0u) * a.ldy + at, n);
+            for (int j = 0; j < kAtOnce; ++j) y[j] = get8<DT, NT>(a.y + (r[j] < a.rows ? r[j] : 0u) * a.ldy + at, n);
 #pragma unroll
             for (int j = 0; j < kAtOnce; ++j) {
                 float v[8];
@@ -90,7 +90,7 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(TokenArgs a, int lp) 
 #pragma unroll
             for (int i = 0; i < 8; ++i) sum[i] = v[i] + sum[i];
         }
-        put8<DT>(a.out + t * a.ldo + at, n, rounded<DT>(sum));
+        put8<DT, NT>(a.out + t * a.ldo + at, n, rounded<DT>(sum));
     }
 }
 
@@ -193,15 +193,19 @@ hipError_t launch_gather_t(const TokenArgs &a, hipStream_t s) {
         hipLaunchKernelGGL((gather_kernel<DT, false>), grid, dim3(kThreads), 0, s, a, lp);
     return hipGetLastError();
 }
-template <int DT>
-hipError_t launch_combine_t(const TokenArgs &a, hipStream_t s) {
+template <int DT, bool DROP>
+hipError_t launch_combine_d(const TokenArgs &a, hipStream_t s) {
     const int lp = lanes_log2(a.dim, 8);
     const dim3 grid = token_grid(a.tokens, lp, a.dim);
-    if (a.drop.bar)
-        hipLaunchKernelGGL((combine_kernel<DT, true>), grid, dim3(kThreads), 0, s, a, lp);
+    if (a.tokens * (a.topk + (a.x ? 2 : 1)) * a.dim * kElem<DT> > kPastCaches)
+        hipLaunchKernelGGL((combine_kernel<DT, DROP, true>), grid, dim3(kThreads), 0, s, a, lp);
     else
-        hipLaunchKernelGGL((combine_kernel<DT, false>), grid, dim3(kThreads), 0, s, a, lp);
+        hipLaunchKernelGGL((combine_kernel<DT, DROP, false>), grid, dim3(kThreads), 0, s, a, lp);
     return hipGetLastError();
+}
+template <int DT>
+hipError_t launch_combine_t(const TokenArgs &a, hipStream_t s) {
+    return a.drop.bar ? launch_combine_d<DT, true>(a, s) : launch_combine_d<DT, false>(a, s);
 }
 template <int J, int DT>
 hipError_t launch_combine_grad_j(const TokenArgs &a, hipStream_t s) {
