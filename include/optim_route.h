@@ -39,7 +39,7 @@ typedef struct optim_route_hp {
                             divides experts, at most 64                     */
     int32_t top_groups;  /* groups of a token, 1 .. groups                  */
     int32_t group_best;  /* a group counts its best one or two: 1 or 2      */
-    double scale;        /* of the weights, finite                          */
+    double scale;        /* of the weights, finite in fp32                  */
 } optim_route_hp;
 
 /* ---- routing -------------------------------------------------------------

@@ -51,7 +51,7 @@ int check_route_hp(const optim_route_hp *hp, int32_t experts) {
     if (hp->group_best != 1 && hp->group_best != 2) return fail(OPTIM_EINVAL, "group_best must be 1 or 2");
     if (hp->topk > experts / hp->groups * hp->top_groups)
         return fail(OPTIM_EINVAL, "topk is above the number of experts in top_groups groups");
-    if (!std::isfinite(hp->scale)) return fail(OPTIM_EINVAL, "scale must be finite");
+    if (!std::isfinite((float)hp->scale)) return fail(OPTIM_EINVAL, "scale must be finite, in fp32 as well");
     return OPTIM_OK;
 }
 

@@ -54,7 +54,7 @@ def test_route(L):
     refuses(call, osa.OPTIM_EINVAL, [dict(hp=h) for h in (
         route_hp(0), route_hp(9), route_hp(33), route_hp(score=2), route_hp(score=-1), route_hp(groups=0), route_hp(groups=3),
         route_hp(groups=2, top_groups=0), route_hp(groups=2, top_groups=3), route_hp(groups=2, group_best=3), route_hp(group_best=0),
-        route_hp(5, groups=2), route_hp(scale=math.nan), route_hp(scale=math.inf))])
+        route_hp(5, groups=2), route_hp(scale=math.nan), route_hp(scale=math.inf), route_hp(scale=1e39))])
     assert call(e=130, ld=130, hp=route_hp(groups=65)) == osa.OPTIM_EINVAL
     refuses(call, osa.OPTIM_EDTYPE, [dict(dt=3), dict(dt=-1)])
     refuses(call, osa.OPTIM_EALIGN, [dict(x=A + 2), dict(idx=A + G + 2), dict(w=A + 2 * G + 1), dict(bias=A + 3 * G + 2),
