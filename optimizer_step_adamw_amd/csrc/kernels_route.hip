@@ -6,6 +6,7 @@
 #include "elems.h"
 
 #include <cfloat>
+#include <type_traits>
 
 namespace optim {
 namespace {
@@ -492,7 +493,8 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, Lay lay) {
         hi = max16(hi);
         lo = min16(lo);
         error = scored ? (error + 2.0f * fmaxf(fabsf(hi), fabsf(lo))) * 0x1p-24f : 0.0f;
-        const float floor = fmaxf(lo, hi - 32.0f);  // choices far below the largest have no place
+        // choices far below the largest have no place
+        const float floor = fmaxf(lo, hi - fmaxf(32.0f, 0.25f * fminf(hi - lo, 4096.0f)));
         const float step = hi > floor ? fminf(kSteps * __builtin_amdgcn_rcpf(hi - floor), FLT_MAX) : 1.0f;
         // ---- keys: place and number, at first the number within the lane; no place
         // (0) for what is not available
@@ -616,6 +618,104 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, Lay lay) {
         redo &= ~(0xFFFFull << (of * 16));
         route_token<V64, DT>(a, t0 + of, lds[wave], lane);
         wave_sync();
+    }
+}
+
+// ---------------------------------------------------------------- a token a lane
+// Few experts: a lane holds a whole row, and nothing passes between lanes.  The
+// choice is made as it is defined, on fp64 keys where there is a bias (BIAS) and on
+// the logits otherwise.
+constexpr int kLaneTopk = 8;
+template <int V, int DT, bool BIAS>
+__global__ __launch_bounds__(kThreads) void route_lane_kernel(RouteArgs a) {
+    using Key = std::conditional_t<BIAS, double, float>;
+    constexpr Key kShut = -(Key)__builtin_inff();
+    const int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (t >= a.tokens) return;
+    const char *row = a.logits + t * a.ldl;
+    float l[V];
+    bool nan = false;
+#pragma unroll
+    for (int q = 0; q < V; q += 8) {
+        const int n = a.experts - q;
+        float x[8] = {};
+        if (n > 0) floats<DT>(get8<DT>(row + q * kElem<DT>, n), x);
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+            l[q + v] = v < n ? x[v] : -INFINITY;
+            nan |= l[q + v] != l[q + v];
+            l[q + v] = tamed(l[q + v]);
+        }
+    }
+    const bool soft = a.score == OPTIM_ROUTE_SOFTMAX;
+    float most = -INFINITY;
+#pragma unroll
+    for (int v = 0; v < V; ++v) most = more_of(most, l[v]);
+    const float from = most > -INFINITY ? most : 0.0f;
+    float total = 0.0f;
+    if (soft && !a.renormalise) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) total += __builtin_amdgcn_exp2f((l[v] - from) * 1.44269504f);
+    }
+    Key key[V];
+    if constexpr (BIAS) {
+        double sum = 0.0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            key[v] = soft ? exp((double)l[v] - from) : 1.0 / (1.0 + exp(-(double)l[v]));
+            sum += key[v];
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const float b = v < a.experts ? a.bias[v] : -INFINITY;
+            key[v] = l[v] > -INFINITY && b > -INFINITY ? (soft ? key[v] / sum : key[v]) + (double)b : kShut;
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) key[v] = l[v];
+    }
+    float mine[kLaneTopk];
+#pragma unroll
+    for (int j = 0; j < kLaneTopk; ++j) {
+        mine[j] = -INFINITY;
+        if (j >= a.topk) continue;
+        Key best = kShut;
+        int32_t at = -1;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const bool more = key[v] > best;
+            best = more ? key[v] : best;
+            at = more ? v : at;
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const bool it = at == v;
+            key[v] = it ? kShut : key[v];
+            mine[j] = it ? l[v] : mine[j];
+        }
+        a.idx[t * a.topk + j] = at;
+    }
+    float w[kLaneTopk], chosen = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < kLaneTopk; ++j) chosen = more_of(chosen, mine[j]);
+    if (a.renormalise) total = 0.0f;
+    else if (!soft) total = 1.0f;
+#pragma unroll
+    for (int j = 0; j < kLaneTopk; ++j) {
+        if (j >= a.topk) continue;
+        if (a.renormalise) {
+            w[j] = part_of_score(a.score, mine[j], chosen);
+            total += w[j];
+        } else {
+            w[j] = !(mine[j] > -INFINITY) ? 0.0f : soft ? expf(mine[j] - from) : sigmoid(mine[j]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < kLaneTopk; ++j) {
+        if (j >= a.topk) continue;
+        float x = mine[j] > -INFINITY ? w[j] / total : 0.0f;
+        x *= a.scale;
+        a.weights[t * a.topk + j] = nan ? __builtin_nanf("") : x;
     }
 }
 
@@ -781,6 +881,20 @@ void launch_route_d(const RouteArgs &a, Lay lay, int dtype, hipStream_t s) {
     if (dtype == OPTIM_BF16) return launch_route_t<V, D, OPTIM_BF16>(a, lay, s);
     launch_route_t<V, D, OPTIM_F16>(a, lay, s);
 }
+template <int V, int DT>
+void launch_route_lane_t(const RouteArgs &a, hipStream_t s) {
+    const dim3 grid((unsigned)((a.tokens + kThreads - 1) / kThreads));
+    if (a.bias)
+        hipLaunchKernelGGL((route_lane_kernel<V, DT, true>), grid, dim3(kThreads), 0, s, a);
+    else
+        hipLaunchKernelGGL((route_lane_kernel<V, DT, false>), grid, dim3(kThreads), 0, s, a);
+}
+template <int V>
+void launch_route_lane(const RouteArgs &a, int dtype, hipStream_t s) {
+    if (dtype == OPTIM_F32) return launch_route_lane_t<V, OPTIM_F32>(a, s);
+    if (dtype == OPTIM_BF16) return launch_route_lane_t<V, OPTIM_BF16>(a, s);
+    launch_route_lane_t<V, OPTIM_F16>(a, s);
+}
 template <int V>
 void launch_route_v(const RouteArgs &a, Lay lay, int dtype, hipStream_t s) {
     if constexpr (V < 64)
@@ -816,7 +930,13 @@ hipError_t launch_route(const RouteArgs &args, int dtype, hipStream_t s) {
     const Lay lay = lay_of(args.experts, args.groups);
     const bool rows16 = args.topk <= (lay.n > 32 ? 15 : 16) &&
                         (args.groups == 1 || (16 % args.groups == 0 && args.experts % 16 == 0));
+    // A lane a token has the shortest way but few wavefronts.  Measured, by lanes and
+    // by 16 lanes a token: 65536 x 8 3.7 and 14 us (with a bias 5.7 and 14), x 16 5.6
+    // and 14; 16384 x 8 3.5 and 5.4 (5.5 and 5.4), x 16 5.3 and 5.4; 8192 x 16 5.2 and
+    // 4.2; 65536 x 32 11.2 (19.7 with a bias) and 13.
+    const bool lanes = args.groups == 1 && args.topk <= kLaneTopk && args.experts <= 16 && args.tokens >= 16384;
     return route_slices(args, [&](const RouteArgs &a) {
+        if (lanes) return a.experts <= 8 ? launch_route_lane<8>(a, dtype, s) : launch_route_lane<16>(a, dtype, s);
         if (rows16) {
             if (lay.n <= 4) return launch_route_v<4>(a, lay, dtype, s);
             if (lay.n <= 8) return launch_route_v<8>(a, lay, dtype, s);

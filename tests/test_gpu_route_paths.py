@@ -108,3 +108,31 @@ def test_few_tokens_leave_what_lies_behind(tokens):
     osa.optim_route_grad(logits, HP(8), idx[:tokens], w[:tokens], d[:tokens])
     assert bool((idx[tokens:] == 77).all()) and bool((w[tokens:] == 77).all()) and bool((d[tokens:] == 77).all())
     assert bool((idx[:tokens] < 64).all()) and torch.equal(d[:tokens], run_grad(logits, HP(8), idx[:tokens], w[:tokens]))
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("experts,topk", [(1, 1), (3, 2), (8, 2), (8, 8), (9, 1), (13, 8), (16, 4)])
+def test_many_tokens_of_few_experts(dtype, experts, topk):
+    """Large batches of few experts have a kernel of their own: the first and last
+    rows against the definition, among them masked ones, infinities and NaN; all
+    of them against the same rows in small batches."""
+    tokens = 16384 + 37
+    logits = normal(experts, tokens, experts).to(DTYPES[dtype])
+    logits[3], logits[4, 0], logits[5, experts - 1], logits[6] = -math.inf, math.nan, math.inf, torch.finfo(DTYPES[dtype]).min
+    logits[7, 1:], logits[8] = -math.inf, 0.0
+    logits[-1, 0] = -math.inf
+    bias = normal(99, experts, std=0.1)
+    some = torch.cat([torch.arange(40), torch.arange(tokens - 40, tokens)]).to(DEV)
+    for hp, b in ((HP(topk, SOFT, 1), None), (HP(topk, SOFT, 0, scale=0.5), None), (HP(topk, SIG, 1), bias), (HP(topk, SOFT, 1), bias),
+                  (HP(topk, SIG, 0), None)):
+        idx, w = run(logits, hp, b)
+        few_idx = check(logits[some].contiguous(), hp, b)
+        few_w = run(logits[some].contiguous(), hp, b)[1]
+        assert torch.equal(idx[some], few_idx)
+        assert torch.allclose(w[some], few_w, rtol=2 * 150 * 2.0 ** -24, atol=1e-37, equal_nan=True)
+        parts = [run(logits[a:a + 8000].contiguous(), hp, b)[0] for a in range(0, tokens, 8000)]
+        assert torch.equal(idx, torch.cat(parts))
+    loose = torch.full((tokens, experts + 3), math.nan, dtype=DTYPES[dtype], device=DEV)
+    loose[:, :experts] = logits
+    a, b = run(logits, HP(topk)), run(loose[:, :experts], HP(topk))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1].view(torch.int32), b[1].view(torch.int32))
