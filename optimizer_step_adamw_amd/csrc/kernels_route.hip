@@ -46,16 +46,31 @@ __device__ __forceinline__ double halves(double x, F &&f) {
     return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
-// The largest key and, of equal ones, the lowest expert, over the wavefront.
+// Within rows of 16 lanes, values pass between lanes without LDS (DPP).  Each of
+// these pairs a lane with one of the other half of its 2, 4, 8 or 16.
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kMirror8 = 0x141, kMirror16 = 0x140, kBroadcast = 0x150, kNext = 0x101;
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t x) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xF, 0xF, true);
+}
+// The larger key and, of equal ones, the lower expert.
+__device__ __forceinline__ void better(double k2, int32_t e2, double &k, int32_t &e) {
+    const bool it = (k2 > k) | ((k2 == k) & (e2 < e));
+    k = it ? k2 : k;
+    e = it ? e2 : e;
+}
+template <int CTRL>
+__device__ __forceinline__ void better_lane(double &k, int32_t &e) {
+    better(halves(k, [](int x) { return (int)dpp<CTRL>((uint32_t)x); }), (int32_t)dpp<CTRL>((uint32_t)e), k, e);
+}
+// The best one of the wavefront.
 __device__ __forceinline__ void wave_best(double &k, int32_t &e) {
-    for (int m = 32; m; m /= 2) {
-        const double k2 = halves(k, [&](int x) { return __shfl_xor(x, m); });
-        const int32_t e2 = __shfl_xor(e, m);
-        if (k2 > k || (k2 == k && e2 < e)) {
-            k = k2;
-            e = e2;
-        }
-    }
+    better_lane<kXor1>(k, e);
+    better_lane<kXor2>(k, e);
+    better_lane<kMirror8>(k, e);
+    better_lane<kMirror16>(k, e);
+#pragma unroll
+    for (int m = 16; m < 64; m *= 2) better(halves(k, [&](int x) { return __shfl_xor(x, m); }), __shfl_xor(e, m), k, e);
 }
 
 // The two largest keys of a group, b0 >= b1.
@@ -101,20 +116,28 @@ __device__ __forceinline__ int32_t choose(const RouteArgs &a, const char *row, d
 #pragma unroll
         for (int v = 0; v < V; ++v) lds[lane + 64 * v] = k[v];
         wave_sync();
+        // `width` lanes a group, a power of two
+        const int32_t width = 64 >> (a.groups > 1 ? 32 - __builtin_clz(a.groups - 1) : 0), mine = lane / width;
         double b0 = kNone, b1 = kNone;
-        if (lane < a.groups)
-            for (int32_t i = 0; i < per; ++i) keep_two(lds[lane * per + i], b0, b1);
+        if (mine < a.groups)
+            for (int32_t i = lane & (width - 1); i < per; i += width) keep_two(lds[mine * per + i], b0, b1);
+        for (int m = 1; m < width; m *= 2) {
+            const double o0 = halves(b0, [&](int x) { return __shfl_xor(x, m); });
+            const double o1 = halves(b1, [&](int x) { return __shfl_xor(x, m); });
+            b1 = fmax(fmin(b0, o0), fmax(b1, o1));
+            b0 = fmax(b0, o0);
+        }
         const double rank = a.group_best > 1 && b1 > kNone ? b0 + b1 : b0;
         int32_t ahead = 0;
         for (int32_t g = 0; g < a.groups; ++g) {
-            const double r = halves(rank, [&](int x) { return __shfl(x, g); });
-            ahead += r > rank || (r == rank && g < lane) ? 1 : 0;
+            const double r = halves(rank, [&](int x) { return __shfl(x, g * width); });
+            ahead += (r > rank) | ((r == rank) & (g < mine)) ? 1 : 0;
         }
-        const uint64_t kept = __ballot(lane < a.groups && ahead < a.top_groups);
+        const uint64_t kept = __ballot(mine < a.groups && ahead < a.top_groups);  // in all of a group's lanes
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int32_t e = lane + 64 * v;
-            if (e < a.experts && !(kept >> (e / per) & 1)) k[v] = kNone;
+            if (e < a.experts && !(kept >> (e / per * width) & 1)) k[v] = kNone;
         }
     }
     int32_t mine = -1;
@@ -198,13 +221,6 @@ __global__ __launch_bounds__(kThreads) void route_wave_kernel(RouteArgs a) {
 }
 
 // ---------------------------------------------------------------- four tokens a wavefront
-// Within rows of 16 lanes, values pass between lanes without LDS (DPP).  Each of
-// these pairs a lane with one of the other half of its 2, 4, 8 or 16.
-constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kMirror8 = 0x141, kMirror16 = 0x140, kBroadcast = 0x150, kNext = 0x101;
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp(uint32_t x) {
-    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xF, 0xF, true);
-}
 template <int CTRL>
 __device__ __forceinline__ float dpp(float x) { return __uint_as_float(dpp<CTRL>(__float_as_uint(x))); }
 // The largest and smallest of numbers that are no NaN (fmaxf and fminf quiet
@@ -392,11 +408,10 @@ __device__ __forceinline__ uint32_t pick(const uint32_t (&x)[N], int at) {
 // at the border, the wavefront chooses again for that token in fp64.
 //
 // Error of a choice c = s + b, in units of 2^-24: a sigmoid 1 / (1 + 2^(-l log2 e))
-// has |l| s (1 - s) 1.5 <= 0.34 from the exponent, half from the exponential, 3 s
-// from the sum and the reciprocal, below 4; a softmax has its terms' |x| + 3, 20
-// from the sum (V + 4 terms one after another, V <= 64: 68) and 3 of itself,
-// below (V + 32) s as |x| e^-x < 1; the sum with b half of itself.  Twice that is
-// allowed for.
+// has s (1 - s) (1.22 |l| + 2) < 0.8 from the exponent and the exponential, 3 s from
+// the sum and the reciprocal, below 4; a softmax has its terms' |x| + 3, the sum's
+// V + 4 roundings one after another (V <= 64) and the terms' mean |x| + 3, and 3
+// of itself, below (V + 32) s as |x| e^-x < 1; the sum with b |c|.
 template <int V, int D, int DT, bool FULL>
 __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, Lay lay) {
     constexpr int V64 = V < 4 ? 1 : V / 4;
@@ -450,7 +465,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, Lay lay) {
                 }
                 total = sum16(total);
                 const float inv = total > 0.0f ? __builtin_amdgcn_rcpf(total) : 0.0f;
-                error = (2.0f * (V + 32)) * inv;
+                error = (float)(V + 32) * inv;
                 if (masked) {
 #pragma unroll
                     for (int v = 0; v < V; ++v) c[v] = c[v] > -INFINITY ? s[v] * inv : -INFINITY;
@@ -460,7 +475,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, Lay lay) {
                 }
             }
         } else if (scored) {
-            error = 8.0f;
+            error = 4.0f;
             if (masked) {
 #pragma unroll
                 for (int v = 0; v < V; ++v)
@@ -492,7 +507,8 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, Lay lay) {
         }
         hi = max16(hi);
         lo = min16(lo);
-        error = scored ? (error + 2.0f * fmaxf(fabsf(hi), fabsf(lo))) * 0x1p-24f : 0.0f;
+        const float rounding = fmaxf(fabsf(hi), fabsf(lo)) * (1.0625f * 0x1p-24f);  // of a sum
+        error = scored ? error * (1.0625f * 0x1p-24f) + rounding : 0.0f;
         // choices far below the largest have no place
         const float floor = fmaxf(lo, hi - fmaxf(32.0f, 0.25f * fminf(hi - lo, 4096.0f)));
         const float step = hi > floor ? fminf(kSteps * __builtin_amdgcn_rcpf(hi - floor), FLT_MAX) : 1.0f;
@@ -546,7 +562,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, Lay lay) {
             if (a.groups <= 2) with(dpp<kMirror8>(b0), dpp<kMirror8>(b1));
             const float mine = sums && b1 > -INFINITY ? b0 + b1 : b0;
             const int32_t lanes = 16 / a.groups, first = l16 & -lanes;
-            const float apart = 4.0f * error;
+            const float apart = 4.0f * (error + rounding);
             int32_t above = 0, near = 0;  // groups ahead for certain; and those that may be
             if (scored) {
                 const float up = mine + apart, down = mine - apart;
@@ -571,7 +587,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, Lay lay) {
         const uint32_t taken = pick<D>(best, l16 & (D - 1));
         const bool mine_is = l16 < a.topk, placed = taken >> kBits;
         if (!whole) {
-            const float far = 2.0f * error * step + 2.0f;  // steps
+            const float far = 2.0f * error * step + 3.0f;  // steps, and what placing rounds
             const uint32_t margin = !scored ? 1u << kBits : far < (float)(1u << (30 - kBits)) ? ((uint32_t)far + 1u) << kBits : 1u << 30;
             uint32_t next = dpp<kNext>(taken);
             if (V < 64 && a.topk == D) {
