@@ -2,7 +2,14 @@
 //
 // A lane takes the elements of one block of the generator, eight neighbours whose
 // places begin at a multiple of eight: one call of the generator, 20 products of
-// 32 bits, for 16 bytes (16-bit types) read and written.
+// 32 bits for eight draws of 16, so that a mask costs less than the 16 or 32 bytes
+// read and written beside it.  (32 bits a draw would double that, for shares finer
+// than 1/65536.)  The mask is nowhere in memory, and no lane needs another's.
+//
+// Bound by HBM: 134M bf16 with residual 124-129 us (805 MB, 6.2-6.5 TB/s), without
+// 90 us for 201M (5.9), 100M fp32 191 us (5.6); 999 elements 2.3 us, the launch.
+// Past the caches (elems.h: NT) where there is a residual and much of it: without
+// one it gains nothing (805 MB 89.7 us, and 87.4 through the caches).
 #include "elems.h"
 
 namespace optim {
@@ -43,8 +50,8 @@ hipError_t launch_dropout_r(const char *x, const char *residual, char *out, int6
     const int64_t blocks = (n + 14) / 8;
     const int64_t g = (blocks + kThreads - 1) / kThreads;
     const dim3 grid((unsigned)(g < (1 << 23) ? g : 1 << 23));
-    if (n * kElem<DT> * (RES ? 3 : 2) > kPastCaches)
-        hipLaunchKernelGGL((dropout_kernel<DT, RES, true>), grid, dim3(kThreads), 0, s, x, residual, out, n, d);
+    if (RES && n * kElem<DT> * 3 > kPastCaches)
+        hipLaunchKernelGGL((dropout_kernel<DT, RES, RES>), grid, dim3(kThreads), 0, s, x, residual, out, n, d);
     else
         hipLaunchKernelGGL((dropout_kernel<DT, RES, false>), grid, dim3(kThreads), 0, s, x, residual, out, n, d);
     return hipGetLastError();

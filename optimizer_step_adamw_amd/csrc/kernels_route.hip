@@ -1,8 +1,20 @@
 // kernels_route.hip -- routing of tokens to experts and its gradient
 // (optim_route, optim_route_grad).
 //
-// One wavefront per token; lane l holds experts l, l + 64, ...  The choice is
-// made on keys in fp64: the score plus the bias, or the logit itself.
+// The choice is defined on fp64 scores, and only few tokens need them: most are
+// chosen on whole numbers made in fp32, sixteen lanes a token, with a bound on what
+// that may have moved; the others again by a wavefront in fp64 (route_token).
+// Many tokens of few experts are taken by a lane each.  A choice without scores is
+// one of logits, exact in either.
+//
+// Bound by the VALU at 256 experts: four tokens cost a wavefront 870 instructions
+// (200 for scores and keys, 100 to sort a lane's keys, 128 to join the lanes'), 24 us
+// of issue for 65536 tokens.  Measured on MI355X: 65536 x 256 fp32, sigmoid, bias, 4
+// of 8 groups, 8 choices 33 us (71 MB), softmax without bias 22, bf16 20; 65536 x 64
+// 14-16, 16384 x 64 bf16 5.3, one token of 256 4.2; by wavefronts in fp64 (groups
+// that are not whole lanes, more than 16 choices) 65536 x 240 in 12 groups 132.  The
+// gradient reads and writes only: of the whole softmax, 65536 x 256 bf16, 17 us (71
+// MB, 4.2 TB/s, partly from the Infinity Cache).
 #include "elems.h"
 
 #include <cfloat>
@@ -79,7 +91,8 @@ __device__ __forceinline__ void keep_two(double k, double &b0, double &b1) {
     b0 = fmax(b0, k);
 }
 
-// Lane j (below topk) returns choice j, or -1.  V: experts of a lane.
+// Lane j (below topk) returns choice j, or -1.  V: experts of a lane, lane l holds
+// experts l, l + 64, ...
 template <int V, int DT>
 __device__ __forceinline__ int32_t choose(const RouteArgs &a, const char *row, double *lds, int lane) {
     double k[V];

@@ -2,8 +2,18 @@
 // (optim_expert_gather, optim_expert_combine, optim_expert_combine_grad).
 //
 // All three go by token: the token's row is read or written once, and the rows
-// of its choices once each.  P lanes share a token, each taking eight neighbouring
-// columns at a time.
+// of its choices once each, whatever their order; by row, every token's row would be
+// read topk times.  A lane takes eight neighbouring columns (16 bytes of a 16-bit
+// row), and a power of two of lanes a token, up to a workgroup; more columns are
+// more workgroups, so that one token of a reply is spread as well.  Sums of a token
+// are a lane's own, in the order of its choices; the weights' gradients are joined
+// over the lanes in a fixed order.
+//
+// Bound by HBM.  Measured on MI355X: gather 16384 x 2048 bf16 to 8 rows each 115 us
+// (604 MB, 5.3 TB/s), combination of 16384 x 4096 bf16 from 2 with residual and
+// dropout 95-99 us (537 MB, 5.5), its gradient for 20001 x 1000 fp16 from 4 69 us
+// (361 MB, 5.2; 104 when each row was asked for behind the one before it); one
+// token of 4096 from 8 3.3 us.
 #include "elems.h"
 
 namespace optim {
