@@ -614,7 +614,8 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, Lay lay) {
             }
             // equal logits are one choice whose order the numbers give
             again |= mine_is && placed && next >> kBits && taken - next < margin && !(hi == lo && !scored);
-            again |= mine_is && !placed && lo < floor;
+            // choices without a place: chosen ones, or as near to one as rounding goes
+            again |= mine_is && lo < floor && (!placed || (scored && taken < margin));
         }
         const int32_t e = mine_is && placed ? (int32_t)(kNumber - (taken & kNumber)) : -1;
         redo = __ballot(again && live);

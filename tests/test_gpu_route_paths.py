@@ -136,3 +136,16 @@ def test_many_tokens_of_few_experts(dtype, experts, topk):
     loose[:, :experts] = logits
     a, b = run(logits, HP(topk)), run(loose[:, :experts], HP(topk))
     assert torch.equal(a[0], b[0]) and torch.equal(a[1].view(torch.int32), b[1].view(torch.int32))
+
+
+@pytest.mark.parametrize("experts,groups", [(64, 1), (256, 8)])
+def test_choices_around_the_lowest_place(experts, groups):
+    """A bias of 64 for one expert and of 32 for the others: their choices lie where
+    a row's places begin, some above and some below by less than fp32 shows."""
+    steps = torch.randint(-40, 40, (400, experts), device=DEV, generator=torch.Generator(device=DEV).manual_seed(12)).float()
+    logits = 0.3 + steps * 2.0 ** -23
+    bias = torch.full((experts,), 32.0, device=DEV)
+    bias[5], bias[6] = 64.0, 0.0
+    for topk in (2, 3, 8):
+        for score in (SIG, SOFT):
+            check(logits, HP(topk, score, 1, groups, max(1, groups // 2), 1), bias)
