@@ -11,10 +11,10 @@
 // (200 for scores and keys, 100 to sort a lane's keys, 128 to join the lanes'), 24 us
 // of issue for 65536 tokens.  Measured on MI355X: 65536 x 256 fp32, sigmoid, bias, 4
 // of 8 groups, 8 choices 33 us (71 MB), softmax without bias 22, bf16 20; 65536 x 64
-// 14-16, 16384 x 64 bf16 5.3, one token of 256 4.2; by wavefronts in fp64 (groups
-// that are not whole lanes, more than 16 choices) 65536 x 240 in 12 groups 132.  The
-// gradient reads and writes only: of the whole softmax, 65536 x 256 bf16, 17 us (71
-// MB, 4.2 TB/s, partly from the Infinity Cache).
+// 14-16, 16384 x 64 bf16 5.3, one token of 256 4.2, 65536 x 240 in 12 groups 58; by
+// wavefronts in fp64 (more than 16 groups, more than 16 choices) 32768 x 512, 17
+// choices, 101.  The gradient reads and writes only: of the whole softmax, 65536 x
+// 256 bf16, 17 us (71 MB, 4.2 TB/s, partly from the Infinity Cache).
 #include "elems.h"
 
 #include <cfloat>
@@ -332,12 +332,23 @@ __device__ __forceinline__ void absorb_lane(uint32_t (&a)[D]) {
     absorb<D>(a, b);
 }
 
-// How a row lies in a token's 16 lanes: lane i holds experts n i ... n i + n - 1.
+// How a row lies in a token's 16 lanes: `lanes` of them, a power of two, have a
+// group of `per` experts, n each but for the last ones.  (Groups are made up to a
+// power of two by empty ones; per <= lanes * n, so that an expert's number and the
+// V - 1 behind it stay below 16 V.)
 struct Lay {
-    int32_t n;
+    int32_t lanes, per, n;
     bool quads;  // four neighbours are one access, all there or none
     bool full;   // every one of the V of every lane is there
 };
+struct Part {
+    int32_t first, n;  // a lane's experts
+};
+__device__ __forceinline__ Part part_of(const RouteArgs &a, const Lay &lay, int l16) {
+    const int32_t g = l16 / lay.lanes, at = (l16 & (lay.lanes - 1)) * lay.n, left = lay.per - at;
+    if (g >= a.groups || left <= 0) return Part{0, 0};
+    return Part{g * lay.per + at, left < lay.n ? left : lay.n};
+}
 template <int DT>
 __device__ __forceinline__ void load4(const char *p, float *x) {
     if constexpr (DT == OPTIM_F32) {
@@ -355,13 +366,12 @@ __device__ __forceinline__ void load4(const char *p, float *x) {
 }
 // This lane's part of a row, `none` where there is no expert.
 template <int V, int DT, bool FULL>
-__device__ __forceinline__ void load_row(const char *row, int32_t experts, Lay lay, int lane, float none, float (&x)[V]) {
-    const int32_t e0 = lane * (FULL ? V : lay.n);
-    if (FULL || lay.quads) {
+__device__ __forceinline__ void load_row(const char *row, Part part, bool quads, float none, float (&x)[V]) {
+    if (FULL || quads) {
 #pragma unroll
         for (int q = 0; q < V; q += 4) {
-            const bool in = FULL || (q < lay.n && e0 + q < experts);
-            load4<DT>(row + (int64_t)(in ? e0 + q : 0) * kElem<DT>, x + q);
+            const bool in = FULL || q < part.n;
+            load4<DT>(row + (int64_t)(in ? part.first + q : 0) * kElem<DT>, x + q);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (!FULL) x[q + i] = in ? x[q + i] : none;
@@ -369,8 +379,8 @@ __device__ __forceinline__ void load_row(const char *row, int32_t experts, Lay l
     } else {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const bool in = v < lay.n && e0 + v < experts;
-            x[v] = logit_at<DT>(row, in ? e0 + v : 0);
+            const bool in = v < part.n;
+            x[v] = logit_at<DT>(row, in ? part.first + v : 0);
             x[v] = in ? x[v] : none;
         }
     }
@@ -436,7 +446,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, Lay lay) {
     const int lane = threadIdx.x & 63, l16 = lane & 15, wave = threadIdx.x >> 6;
     const bool sums = a.groups > 1 && a.group_best > 1, scored = a.bias || sums;
     const bool whole = DT != OPTIM_F32 && !scored;  // exact keys
-    const int32_t e0 = l16 * (FULL ? V : lay.n);
+    const Part part = FULL ? Part{l16 * V, V} : part_of(a, lay, l16);
     const int64_t t0 = ((int64_t)blockIdx.x * kWaves + wave) * 4;
     if (t0 >= a.tokens) return;
     uint64_t redo;
@@ -445,8 +455,8 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, Lay lay) {
         const bool live = t < a.tokens;
         const char *row = a.logits + (live ? t : t0) * a.ldl;
         float c[V], b[V];
-        load_row<V, DT, FULL>(row, a.experts, lay, l16, -INFINITY, c);
-        if (a.bias) load_row<V, OPTIM_F32, FULL>(reinterpret_cast<const char *>(a.bias), a.experts, lay, l16, -INFINITY, b);
+        load_row<V, DT, FULL>(row, part, lay.quads, -INFINITY, c);
+        if (a.bias) load_row<V, OPTIM_F32, FULL>(reinterpret_cast<const char *>(a.bias), part, lay.quads, -INFINITY, b);
         // (in every lane) some expert may not be available
         bool masked = !FULL || !all_finite(c), nan = false;
         if (masked) {
@@ -528,7 +538,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, Lay lay) {
         // ---- keys: place and number, at first the number within the lane; no place
         // (0) for what is not available
         uint32_t key[V];
-        const uint32_t number = kNumber - (uint32_t)e0 - (V - 1);
+        const uint32_t number = kNumber - (uint32_t)part.first - (V - 1);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             uint32_t place;
@@ -557,7 +567,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, Lay lay) {
         }
 #pragma unroll
         for (int i = 0; i < D; ++i) best[i] += number;
-        // ---- groups: 16 / groups lanes each
+        // ---- groups
         bool again = false, kept = true;
         if (a.groups > 1) {
             float b0 = -INFINITY, b1 = -INFINITY;
@@ -570,11 +580,11 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, Lay lay) {
                 b1 = most_of(less_of(b0, o0), b1, o1);
                 b0 = more_of(b0, o0);
             };
-            if (a.groups <= 8) with(dpp<kXor1>(b0), dpp<kXor1>(b1));
-            if (a.groups <= 4) with(dpp<kXor2>(b0), dpp<kXor2>(b1));
-            if (a.groups <= 2) with(dpp<kMirror8>(b0), dpp<kMirror8>(b1));
+            const int32_t lanes = lay.lanes, first = l16 & -lanes;
+            if (lanes >= 2) with(dpp<kXor1>(b0), dpp<kXor1>(b1));
+            if (lanes >= 4) with(dpp<kXor2>(b0), dpp<kXor2>(b1));
+            if (lanes >= 8) with(dpp<kMirror8>(b0), dpp<kMirror8>(b1));
             const float mine = sums && b1 > -INFINITY ? b0 + b1 : b0;
-            const int32_t lanes = 16 / a.groups, first = l16 & -lanes;
             const float apart = 4.0f * (error + rounding);
             int32_t above = 0, near = 0;  // groups ahead for certain; and those that may be
             if (scored) {
@@ -583,7 +593,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, Lay lay) {
                     above += r > up;
                     near += r >= down;
                 });
-                near -= mine > -INFINITY ? 1 : a.groups;  // itself
+                near -= mine > -INFINITY ? 1 : 16 / lanes;  // itself
             } else {
                 each16(lanes, mine, [&](int i, float r) { near += (r > mine) | ((r == mine) & (i < first)); });
             }
@@ -931,13 +941,15 @@ void launch_route_v(const RouteArgs &a, Lay lay, int dtype, hipStream_t s) {
         if (a.topk <= 8) return launch_route_d<V, 8>(a, lay, dtype, s);
     launch_route_d<V, 16>(a, lay, dtype, s);
 }
-// Experts of a lane of 16.  Groups are whole lanes; without them fours are kept
-// together.
 Lay lay_of(int32_t experts, int32_t groups) {
-    const int32_t n = (experts + 15) / 16;
-    const int32_t each = groups > 1 ? n : (n + 3) / 4 * 4;
-    return Lay{each, each % 4 == 0 && experts % 4 == 0, false};
+    int32_t lanes = 16;
+    while (lanes > 1 && 16 / lanes < groups) lanes /= 2;
+    const int32_t per = experts / groups, n = (per + lanes - 1) / lanes;
+    // fours are kept together where that makes them single accesses
+    const bool quads = per % 4 == 0;
+    return Lay{lanes, per, quads ? (n + 3) / 4 * 4 : n, quads, false};
 }
+
 template <int L, int C, int DT>
 void launch_route_grad_t(const RouteGradArgs &a, hipStream_t s) {
     constexpr int64_t kTokens = kWaves * 64 / L;
@@ -958,8 +970,7 @@ void launch_route_grad_c(const RouteGradArgs &a, int dtype, hipStream_t s) {
 
 hipError_t launch_route(const RouteArgs &args, int dtype, hipStream_t s) {
     const Lay lay = lay_of(args.experts, args.groups);
-    const bool rows16 = args.topk <= (lay.n > 32 ? 15 : 16) &&
-                        (args.groups == 1 || (16 % args.groups == 0 && args.experts % 16 == 0));
+    const bool rows16 = args.topk <= (lay.n > 32 ? 15 : 16) && args.groups <= 16 && lay.n <= 64;
     // A lane a token has the shortest way but few wavefronts.  Measured, by lanes and
     // by 16 lanes a token: 65536 x 8 3.7 and 14 us (with a bias 5.7 and 14), x 16 5.6
     // and 14; 16384 x 8 3.5 and 5.4 (5.5 and 5.4), x 16 5.3 and 5.4; 8192 x 16 5.2 and

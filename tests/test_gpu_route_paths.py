@@ -149,3 +149,20 @@ def test_choices_around_the_lowest_place(experts, groups):
     for topk in (2, 3, 8):
         for score in (SIG, SOFT):
             check(logits, HP(topk, score, 1, groups, max(1, groups // 2), 1), bias)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("experts,groups", [(9, 3), (36, 12), (75, 5), (90, 2), (90, 3), (130, 13), (136, 8), (210, 14), (248, 8), (252, 6),
+                                            (340, 17), (504, 8), (1008, 16), (1020, 12), (1023, 3), (1023, 11)])
+def test_groups_of_any_size(dtype, experts, groups):
+    logits = normal(experts + groups, 37, experts).to(DTYPES[dtype])
+    logits[4, :experts // groups] = -math.inf  # a group without any
+    logits[5, experts // groups:] = -math.inf  # one group alone
+    bias = normal(experts, experts, std=0.1)
+    for top_groups in (1, max(1, groups // 2), groups):
+        topk = min(8, experts // groups * top_groups)
+        for score in (SOFT, SIG):
+            check(logits, HP(topk, score, 1, groups, top_groups, 2), bias)
+            check(logits, HP(topk, score, 0, groups, top_groups, 1), bias)
+        check(logits, HP(topk, SIG, 1, groups, top_groups, 1))
+        check(logits, HP(min(16, experts // groups * top_groups), SOFT, 1, groups, top_groups, 1))
