@@ -589,13 +589,22 @@ def optim_route_rows(idx, offsets, place, *, order=None, workspace=None, stream=
 
 def _token_shapes(place, by_token, by_row):
     """(tokens, topk, dim, rows) of matrices by token and by row."""
-    t, k = place.shape if place.dim() == 2 else (-1, 0)
-    by_token, by_row = [m.shape for m in by_token if m is not None], [m.shape for m in by_row if m is not None]
-    dim, rows = (by_token[0] or (0,))[-1], (by_row[0] or (0,))[0]
-    if any(s != (t, dim) for s in by_token) or any(s != (rows, dim) for s in by_row):
-        raise ValueError(f"shapes do not fit: by token {[tuple(s) for s in by_token]}, by row {[tuple(s) for s in by_row]}, "
-                         f"place {tuple(place.shape)}")
-    return t, k, dim, rows
+    at, dim, rows = place.shape, -1, -1
+    fits = len(at) == 2
+    for m in by_token:
+        if m is not None:
+            s = m.shape
+            fits = fits and len(s) == 2 and s[0] == at[0] and (dim < 0 or s[1] == dim)
+            dim = s[-1] if fits else dim
+    for m in by_row:
+        if m is not None:
+            s = m.shape
+            fits = fits and len(s) == 2 and s[1] == dim and (rows < 0 or s[0] == rows)
+            rows = s[0] if fits else rows
+    if not fits:
+        raise ValueError(f"shapes do not fit: by token {[tuple(m.shape) for m in by_token if m is not None]}, by row "
+                         f"{[tuple(m.shape) for m in by_row if m is not None]}, place {tuple(at)}")
+    return at[0], at[1], dim, rows
 
 
 def optim_expert_gather(x, place, y, *, weights=None, stream=None) -> None:

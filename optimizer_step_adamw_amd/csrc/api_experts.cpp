@@ -72,6 +72,7 @@ int check_drop(const optim_dropout_hp *hp, const int32_t *step_dev, DropArgs &d)
 
 struct Ranges {
     std::vector<Range> all;
+    Ranges() { all.reserve(8); }
     void add(const void *p, size_t bytes, bool written, const char *what) {
         if (p && bytes) all.push_back({(uintptr_t)p, (uintptr_t)p + bytes, written, 0, what});
     }

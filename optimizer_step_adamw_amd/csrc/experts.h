@@ -52,7 +52,7 @@ struct RowsArgs {
     int32_t *counts;                   // [blocks], rows_workspace() bytes; NULL where one block does it all
     int32_t n, experts, chunk, blocks;
 };
-// Choices a workgroup takes, a multiple of 512, and workgroups.
+// Choices a workgroup takes, a multiple of 1024, and workgroups.
 struct RowsShape {
     int32_t chunk, blocks;
 };

@@ -237,25 +237,27 @@ __global__ __launch_bounds__(kThreads) void route_wave_kernel(RouteArgs a) {
 template <int CTRL>
 __device__ __forceinline__ float dpp(float x) { return __uint_as_float(dpp<CTRL>(__float_as_uint(x))); }
 // The largest and smallest of numbers that are no NaN (fmaxf and fminf quiet
-// each argument first).
+// each argument first).  The wait state is for an argument that a reciprocal or
+// an exponential has just made, which the compiler sees to for its own
+// instructions only.
 __device__ __forceinline__ float most_of(float x, float y, float z) {
     float r;
-    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(x), "v"(y), "v"(z));
+    asm("s_nop 0\n\tv_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(x), "v"(y), "v"(z));
     return r;
 }
 __device__ __forceinline__ float least_of(float x, float y, float z) {
     float r;
-    asm("v_min3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(x), "v"(y), "v"(z));
+    asm("s_nop 0\n\tv_min3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(x), "v"(y), "v"(z));
     return r;
 }
 __device__ __forceinline__ float more_of(float x, float y) {
     float r;
-    asm("v_max_f32 %0, %1, %2" : "=v"(r) : "v"(x), "v"(y));
+    asm("s_nop 0\n\tv_max_f32 %0, %1, %2" : "=v"(r) : "v"(x), "v"(y));
     return r;
 }
 __device__ __forceinline__ float less_of(float x, float y) {
     float r;
-    asm("v_min_f32 %0, %1, %2" : "=v"(r) : "v"(x), "v"(y));
+    asm("s_nop 0\n\tv_min_f32 %0, %1, %2" : "=v"(r) : "v"(x), "v"(y));
     return r;
 }
 
@@ -396,7 +398,7 @@ __device__ __forceinline__ bool all_finite(const float (&x)[V]) {
 }
 
 // The whole part; 0 of what is negative, -inf or NaN (which the language leaves
-// open, and the instruction does not).
+// open, and the instruction does not).  x: an fma's result.
 __device__ __forceinline__ uint32_t whole_part(float x) {
     uint32_t u;
     asm("v_cvt_u32_f32 %0, %1" : "=v"(u) : "v"(x));
