@@ -366,26 +366,29 @@ __device__ __forceinline__ void load4(const char *p, float *x) {
         }
     }
 }
-// This lane's part of a row, `none` where there is no expert.
-template <int V, int DT, bool FULL>
-__device__ __forceinline__ void load_row(const char *row, Part part, bool quads, float none, float (&x)[V]) {
+// Four of this lane's part of a row, from the q-th on; `none` where there is no
+// expert.
+template <int DT, bool FULL>
+__device__ __forceinline__ void load_four(const char *row, Part part, bool quads, int q, float none, float *x) {
     if (FULL || quads) {
+        const bool in = FULL || q < part.n;
+        load4<DT>(row + (int64_t)(in ? part.first + q : 0) * kElem<DT>, x);
 #pragma unroll
-        for (int q = 0; q < V; q += 4) {
-            const bool in = FULL || q < part.n;
-            load4<DT>(row + (int64_t)(in ? part.first + q : 0) * kElem<DT>, x + q);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (!FULL) x[q + i] = in ? x[q + i] : none;
-        }
+        for (int i = 0; i < 4; ++i)
+            if (!FULL) x[i] = in ? x[i] : none;
     } else {
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const bool in = v < part.n;
-            x[v] = logit_at<DT>(row, in ? part.first + v : 0);
-            x[v] = in ? x[v] : none;
+        for (int i = 0; i < 4; ++i) {
+            const bool in = q + i < part.n;
+            x[i] = logit_at<DT>(row, in ? part.first + q + i : 0);
+            x[i] = in ? x[i] : none;
         }
     }
+}
+template <int V, int DT, bool FULL>
+__device__ __forceinline__ void load_row(const char *row, Part part, bool quads, float none, float (&x)[V]) {
+#pragma unroll
+    for (int q = 0; q < V; q += 4) load_four<DT, FULL>(row, part, quads, q, none, x + q);
 }
 
 // Whether a sum of the numbers is finite in every lane: then so are they.
@@ -611,6 +614,8 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, Lay lay) {
         // ---- lane j takes choice j; are neighbours far enough apart?
         const uint32_t taken = pick<D>(best, l16 & (D - 1));
         const bool mine_is = l16 < a.topk, placed = taken >> kBits;
+        const int32_t e = mine_is && placed ? (int32_t)(kNumber - (taken & kNumber)) : -1;
+        const float mine = e >= 0 ? tamed(logit_at<DT>(row, e)) : -INFINITY;
         if (!whole) {
             const float far = 2.0f * error * step + 3.0f;  // steps, and what placing rounds
             const uint32_t margin = !scored ? 1u << kBits : far < (float)(1u << (30 - kBits)) ? ((uint32_t)far + 1u) << kBits : 1u << 30;
@@ -624,16 +629,40 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, Lay lay) {
                 behind = join16(behind, [](uint32_t x, uint32_t y) { return x < y ? x : y; });
                 next = l16 == D - 1 ? best[D - 1] - 1u - behind : next;
             }
-            // equal logits are one choice whose order the numbers give
-            again |= mine_is && placed && next >> kBits && taken - next < margin && !(hi == lo && !scored);
+            bool near = mine_is && placed && next >> kBits && taken - next < margin && !(hi == lo && !scored);
+            // Equal logits (and bias) are one choice, whose order the numbers give: as
+            // often as not where logits have passed through 16 bits.  The chosen ones
+            // are compared each with the next; with the last one, all others as near.
+            if (__any(near)) {
+                const int from = (lane & 48) + a.topk - 1;  // the last one's lane
+                const float with = a.bias && e >= 0 ? tamed(gp(a.bias)[e]) : 0.0f;
+                const float mine2 = dpp<kNext>(mine), with2 = dpp<kNext>(with);
+                const uint32_t least = (uint32_t)__shfl((int)taken, from);
+                const float mine_k = __shfl(mine, from), with_k = __shfl(with, from);
+                const uint32_t last = least - 1u - number;
+                bool other = false;
+#pragma unroll
+                for (int q = 0; q < V; q += 4) {  // (of the keys behind the last one's)
+                    float l[4], b4[4] = {};
+                    load_four<DT, FULL>(row, part, lay.quads, q, -INFINITY, l);
+                    if (a.bias) load_four<OPTIM_F32, FULL>(reinterpret_cast<const char *>(a.bias), part, lay.quads, q, -INFINITY, b4);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        other |= last - key[q + i] < margin && key[q + i] >> kBits != 0u &&
+                                 (tamed(l[i]) != mine_k || (a.bias && tamed(b4[i]) != with_k));
+                    __builtin_amdgcn_sched_barrier(0);  // four at a time: no registers for more
+                }
+                other &= kept;
+                const uint64_t others = __ballot(other);
+                near = near && (l16 == a.topk - 1 ? (others >> (lane & 48) & 0xFFFFull) != 0u : mine != mine2 || with != with2);
+            }
+            again |= near;
             // choices without a place: chosen ones, or as near to one as rounding goes
             again |= mine_is && lo < floor && (!placed || (scored && taken < margin));
         }
-        const int32_t e = mine_is && placed ? (int32_t)(kNumber - (taken & kNumber)) : -1;
         redo = __ballot(again && live);
         const bool sure = !(redo >> (lane & 48) & 0xFFFFull);
         // ---- weights
-        const float mine = e >= 0 ? tamed(logit_at<DT>(row, e)) : -INFINITY;
         float w;
         if (a.renormalise) {
             if (!soft && !__any(mine < -16.0f && e >= 0))  // (off by 28 x 2^-24 at most)

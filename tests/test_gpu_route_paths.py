@@ -166,3 +166,20 @@ def test_groups_of_any_size(dtype, experts, groups):
             check(logits, HP(topk, score, 0, groups, top_groups, 1), bias)
         check(logits, HP(topk, SIG, 1, groups, top_groups, 1))
         check(logits, HP(min(16, experts // groups * top_groups), SOFT, 1, groups, top_groups, 1))
+
+
+@pytest.mark.parametrize("experts,topk", [(12, 5), (64, 6), (64, 8), (256, 8), (256, 16), (300, 8)])
+@pytest.mark.parametrize("score", [SOFT, SIG])
+def test_logits_that_passed_through_16_bits(experts, topk, score):
+    """Many equal logits in fp32 and in bf16, without a bias, with none so far and
+    with one of a few levels; among them rows with a choice nearly equal to others."""
+    logits = normal(31, 60, experts).to(torch.bfloat16).float()
+    logits[::4] = logits[::4].round()
+    logits[1::8, 3] = torch.nextafter(logits[1::8, 2], torch.full((), 9.0, device=DEV))
+    logits[5, 4:] = -math.inf
+    levels = torch.randint(-2, 3, (experts,), device=DEV, generator=torch.Generator(device=DEV).manual_seed(5)).float() * 1e-3
+    for bias in (None, torch.zeros(experts, device=DEV), levels):
+        check(logits, HP(topk, score, 1), bias)
+        check(logits.to(torch.bfloat16), HP(topk, score, 0), bias)
+        if experts % 4 == 0:
+            check(logits, HP(min(topk, experts // 2), score, 1, 4, 2, 1), bias)
