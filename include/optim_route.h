@@ -12,7 +12,7 @@
  * gather), optim_route_grad; and before the next step optim_step_route_bias.
  * Nothing of it reads the device back.
  *
- * Sizes everywhere: tokens * topk < 2^31, topk in [1, 32] and at most experts,
+ * Sizes everywhere: tokens * topk < 2^31, topk in [1, 32],
  * experts in [1, 1024], dim < 2^24, distances between rows below 2^24
  * elements and at least the row's length.  No written array may overlap
  * another array of the call, each from its first element to its last, but where
