@@ -126,18 +126,24 @@ __global__ __launch_bounds__(kThreads) void combine_grad_kernel(TokenArgs a, int
                 w[j] = a.weights ? a.weights[of] : 1.0f;
                 dot[j] = 0.0f;
             }
+            // (a choice without a row reads another one of the token's, which no other
+            // lane writes where dy is y)
+            uint32_t own = ~0u;
+#pragma unroll
+            for (int j = 0; j < J; ++j) own = r[j] < a.rows ? r[j] : own;
+            const bool reads = a.dweights && own < a.rows;
             for (int32_t c = l; live && c < chunks; c += per) {
                 const int n = a.dim - c * 8;
                 const int64_t at = (int64_t)c * (8 * kElem<DT>);
                 const Raw8<DT> dout = get8<DT>(a.x + t * a.ldx + at, n);
                 Raw8<DT> y[J];
-                if (a.dweights && a.rows > 0)
+                if (reads)
 #pragma unroll
-                    for (int j = 0; j < J; ++j) y[j] = get8<DT>(a.y + (r[j] < a.rows ? r[j] : 0u) * a.ldy + at, n);
+                    for (int j = 0; j < J; ++j) y[j] = get8<DT>(a.y + (r[j] < a.rows ? r[j] : own) * a.ldy + at, n);
                 float d[8];
                 floats<DT>(dout, d);
                 if constexpr (DROP) drop8(a.drop, step, (uint64_t)(a.drop.first + t * a.dim + c * 8), d);
-                if (a.dweights && a.rows > 0)
+                if (reads)
 #pragma unroll
                     for (int j = 0; j < J; ++j) {
                         float v[8];
