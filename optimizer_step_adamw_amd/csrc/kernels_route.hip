@@ -618,7 +618,8 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, Lay lay) {
         const float mine = e >= 0 ? tamed(logit_at<DT>(row, e)) : -INFINITY;
         if (!whole) {
             const float far = 2.0f * error * step + 3.0f;  // steps, and what placing rounds
-            const uint32_t margin = !scored ? 1u << kBits : far < (float)(1u << (30 - kBits)) ? ((uint32_t)far + 1u) << kBits : 1u << 30;
+            // (places have at most 32 - kBits bits; a bound past them all makes every two near)
+            const uint32_t margin = !scored ? 1u << kBits : far < (float)((1u << (32 - kBits)) - 2u) ? ((uint32_t)far + 1u) << kBits : ~0u;
             uint32_t next = dpp<kNext>(taken);
             if (V < 64 && a.topk == D) {
                 const uint32_t last = best[D - 1] - 1u - number;
