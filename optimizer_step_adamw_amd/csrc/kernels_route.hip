@@ -591,6 +591,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, Lay lay) {
             if (lanes >= 8) with(dpp<kMirror8>(b0), dpp<kMirror8>(b1));
             const float mine = sums && b1 > -INFINITY ? b0 + b1 : b0;
             const float apart = 4.0f * (error + rounding);
+            const bool open = b0 > -INFINITY;  // (two biases may add up to less than any float)
             int32_t above = 0, near = 0;  // groups ahead for certain; and those that may be
             if (scored) {
                 const float up = mine + apart, down = mine - apart;
@@ -598,12 +599,12 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, Lay lay) {
                     above += r > up;
                     near += r >= down;
                 });
-                near -= mine > -INFINITY ? 1 : 16 / lanes;  // itself
+                near -= open ? 1 : 16 / lanes;  // itself
             } else {
                 each16(lanes, mine, [&](int i, float r) { near += (r > mine) | ((r == mine) & (i < first)); });
             }
             kept = near < a.top_groups;
-            again = scored && !kept && above < a.top_groups && mine > -INFINITY;
+            again = scored && !kept && above < a.top_groups && open;
 #pragma unroll
             for (int i = 0; i < D; ++i) best[i] = kept ? best[i] : 0u;
         }
