@@ -637,7 +637,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, Lay lay) {
             // are compared each with the next; with the last one, all others as near.
             if (__any(near)) {
                 const int from = (lane & 48) + a.topk - 1;  // the last one's lane
-                const float with = a.bias && e >= 0 ? tamed(gp(a.bias)[e]) : 0.0f;
+                const float with = a.bias && e >= 0 ? gp(a.bias)[e] : 0.0f;  // (+inf is not the largest float here)
                 const float mine2 = dpp<kNext>(mine), with2 = dpp<kNext>(with);
                 const uint32_t least = (uint32_t)__shfl((int)taken, from);
                 const float mine_k = __shfl(mine, from), with_k = __shfl(with, from);
@@ -651,7 +651,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, Lay lay) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         other |= last - key[q + i] < margin && key[q + i] >> kBits != 0u &&
-                                 (tamed(l[i]) != mine_k || (a.bias && tamed(b4[i]) != with_k));
+                                 (tamed(l[i]) != mine_k || (a.bias && b4[i] != with_k));
                     __builtin_amdgcn_sched_barrier(0);  // four at a time: no registers for more
                 }
                 other &= kept;
