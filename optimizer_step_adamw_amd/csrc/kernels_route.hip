@@ -859,10 +859,29 @@ __global__ __launch_bounds__(kThreads) void route_grad_kernel(RouteGradArgs a) {
         const float s = mine > -INFINITY ? expf(mine - from) * inv : 0.0f;
         d = g * s;
         const float by = -(lanes_sum<L>(d) * inv);
+        // More than half of the score is one expert's, the only one whose term is 1: its
+        // s (g - sum of g s) would be a difference of nearly equal numbers, and is
+        // s (g (1 - s) - sum over the others of g s), 1 - s from their terms.
+        const bool top = mine == from && s > 0.5f;
+        if (__any(top)) {
+            float rest = 0.0f;
 #pragma unroll
-        for (int i = 0; i < C; ++i)
+            for (int i = 0; i < C; ++i)
 #pragma unroll
-            for (int v = 0; v < 8; ++v) x[i][v] = x[i][v] * by;
+                for (int v = 0; v < 8; ++v) rest += x[i][v] < 1.0f ? x[i][v] : 0.0f;
+            rest = lanes_sum<L>(rest);
+            const float by_top = lanes_max<L>(top ? 1.0f : 0.0f) > 0.0f ? -(lanes_sum<L>(top ? 0.0f : d) * inv) : by;
+            d = top ? d * (rest * inv) : d;
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+#pragma unroll
+                for (int v = 0; v < 8; ++v) x[i][v] = x[i][v] * (x[i][v] < 1.0f ? by : by_top);
+        } else {
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+#pragma unroll
+                for (int v = 0; v < 8; ++v) x[i][v] = x[i][v] * by;
+        }
     } else if (a.renormalise) {
         const float s = part_of_score(a.score, mine, lanes_max<L>(mine));
         const float total = lanes_sum<L>(s);
