@@ -887,6 +887,11 @@ __global__ __launch_bounds__(kThreads) void route_grad_kernel(RouteGradArgs a) {
         const float total = lanes_sum<L>(s);
         const float w = total > 0.0f ? s / total : 0.0f;
         d = w * (g - lanes_sum<L>(g * w));
+        const bool top = w > 0.5f;  // (as above; one lane at most)
+        if (__any(top)) {
+            const float rest = lanes_sum<L>(top ? 0.0f : s), others = lanes_sum<L>(top ? 0.0f : g * w);
+            d = top ? w * (g * (rest / total) - others) : d;
+        }
         if (a.score == OPTIM_ROUTE_SIGMOID) d = d * sigmoid(-mine);
     } else {
         d = g * sigmoid(mine) * sigmoid(-mine);
