@@ -74,7 +74,9 @@ int optim_route(const void *logits_dev, int64_t ldl, int32_t dtype, int64_t toke
  *   sigmoid:               dl_e = [e = idx_j] g_j s_e (1 - s_e)
  *   sigmoid, renormalised: dl_e = [e = idx_j] w_j (1 - s_e) (g_j - sum_j g_j w_j)
  * An expert named twice in a row counts twice.  Only the first form reads more
- * of the logits than the chosen ones.  Not available experts have gradient 0.  */
+ * of the logits than the chosen ones.  An expert whose logit is -inf or NaN has
+ * gradient 0, and a NaN changes no other one's; the bias is not in the scores, so
+ * an expert that only its bias shuts has its s_e in the first form.           */
 int optim_route_grad(const void *logits_dev, int64_t ldl, int32_t dtype, int64_t tokens,
                      int32_t experts, const optim_route_hp *hp, const int32_t *idx_dev,
                      const float *dweights_dev, void *dlogits_dev, int64_t ldd, void *stream);
