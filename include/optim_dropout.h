@@ -21,9 +21,13 @@ extern "C" {
  *   key     (seed mod 2^32, seed div 2^32)
  * word (q mod 8) div 2, its low half for even q, its high half for odd q.
  * Steps that are counted on the device (the step_dev of a plan's calls) thus
- * draw anew at every replay of a captured graph, and a tensor in pieces, or
- * one sharded over ranks, has the mask of the whole where each piece says
- * where it begins.  An element is dropped where r(q) < bar,
+ * draw anew at every replay of a captured graph that moves the count, and a tensor
+ * in pieces, or one sharded over ranks, has the mask of the whole where each piece
+ * says where it begins.  All calls of one step, site and first have one mask:
+ * micro-batches whose gradients one step takes are pieces too, and each says where
+ * it begins (micro-batch i of n elements: i * n); so do ranks with batches of their
+ * own.  A step that is skipped (found_inf) is not counted, and the next one draws
+ * the same again.  An element is dropped where r(q) < bar,
  *   bar = min(65535, floor(65536 p + 1/2)),
  * and is otherwise x * (65536 / (65536 - bar)), the factor rounded to fp32:
  * the mean is x's for every p.  The mask does not depend on type, alignment

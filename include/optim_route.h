@@ -59,7 +59,11 @@ typedef struct optim_route_hp {
  * where fewer than topk are left the remaining idx are -1 with weight 0 (a
  * token all of whose logits are -inf, as in a padded batch, goes nowhere).  A
  * NaN logit makes its row's weights NaN.  A logit of +inf counts as the largest
- * float.                                                                   */
+ * float; a bias of +inf is above every float.  Weights are fp32 throughout, with
+ * the hardware's exponential and reciprocal: off by less than
+ *   u = (2.3 r + experts / 16 + 64) 2^-24
+ * of themselves, r the distance between the row's largest and smallest finite
+ * logit (those below 1e-37 by as much as that).                             */
 int optim_route(const void *logits_dev, int64_t ldl, int32_t dtype, int64_t tokens,
                 int32_t experts, const float *bias_dev, const optim_route_hp *hp,
                 int32_t *idx_dev, float *weights_dev, void *stream);
@@ -76,7 +80,9 @@ int optim_route(const void *logits_dev, int64_t ldl, int32_t dtype, int64_t toke
  * An expert named twice in a row counts twice.  Only the first form reads more
  * of the logits than the chosen ones.  An expert whose logit is -inf or NaN has
  * gradient 0, and a NaN changes no other one's; the bias is not in the scores, so
- * an expert that only its bias shuts has its s_e in the first form.           */
+ * an expert that only its bias shuts has its s_e in the first form.  Each element
+ * is fp32, off by less than 2 u (above) of the sum of its terms' magnitudes, where
+ * g_e s_e (1 - s_e) counts as one term, and then rounded once to the logits' dtype. */
 int optim_route_grad(const void *logits_dev, int64_t ldl, int32_t dtype, int64_t tokens,
                      int32_t experts, const optim_route_hp *hp, const int32_t *idx_dev,
                      const float *dweights_dev, void *dlogits_dev, int64_t ldd, void *stream);
