@@ -7,9 +7,11 @@
 // than 1/65536.)  The mask is nowhere in memory, and no lane needs another's.
 //
 // Bound by HBM: 134M bf16 with residual 124-129 us (805 MB, 6.2-6.5 TB/s), without
-// 90 us for 201M (5.9), 100M fp32 191 us (5.6); 999 elements 2.3 us, the launch.
-// Past the caches (elems.h: NT) where there is a residual and much of it: without
-// one it gains nothing (805 MB 89.7 us, and 87.4 through the caches).
+// one 88-90 us (537 MB, 6.0), 201M 132 (805 MB, 6.1), 134M fp32 184-187 us (1074 MB,
+// 5.8); 999 elements 2.5 us, the launch.  Past the caches (elems.h: NT) where there is
+// a residual and much of it: without one it gains nothing (537 MB bf16 88.6-92.7 us
+// past them, 89.3-89.8 through them, 805 MB 132.0-133.3 and 131.6-132.0, 1074 MB
+// fp32 189 and 186).
 #include "elems.h"
 
 namespace optim {

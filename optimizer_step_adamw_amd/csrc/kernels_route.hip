@@ -7,14 +7,20 @@
 // Many tokens of few experts are taken by a lane each.  A choice without scores is
 // one of logits, exact in either.
 //
-// Bound by the VALU at 256 experts: four tokens cost a wavefront 870 instructions
-// (200 for scores and keys, 100 to sort a lane's keys, 128 to join the lanes'), 24 us
-// of issue for 65536 tokens.  Measured on MI355X: 65536 x 256 fp32, sigmoid, bias, 4
-// of 8 groups, 8 choices 33 us (71 MB), softmax without bias 22, bf16 20; 65536 x 64
-// 14-16, 16384 x 64 bf16 5.3, one token of 256 4.2, 65536 x 240 in 12 groups 58; by
-// wavefronts in fp64 (more than 16 groups, more than 16 choices) 32768 x 512, 17
-// choices, 101.  The gradient reads and writes only: of the whole softmax, 65536 x
-// 256 bf16, 17 us (71 MB, 4.2 TB/s, partly from the Infinity Cache).
+// Bound by the VALU at 256 experts: four tokens cost a wavefront some 880
+// instructions, 24 us of issue for 65536 tokens.  By the assembly, with groups and a
+// bias: loads and their checks 50, sigmoids 64, bias 32, the row's range 60, keys 80,
+// sorting a lane's 115, groups 160, joining the lanes' lists 130, a lane's own choice
+// out of them 105 (the compiler makes comparisons with every index of it), neighbours
+// 60, weights 30.  Measured on MI355X, 8 choices of 65536 tokens, us: fp32, sigmoid,
+// bias, 4 of 8 groups, 256 experts 33 (71 MB), 512 56, 1024 210-218, 240 experts in
+// 12 groups 76-80; softmax without bias, 32 experts 16, 64 14-15, 128 17, 255 37,
+// 256 21, 512 35-36, 1024 146, bf16 64 13-14 and 256 20; 16384 x 64 bf16 5.1-6.0, one
+// token of 256 3.7-4.1; by wavefronts in fp64 (more than 16 groups, more than 16
+// choices) 32768 x 512, 17 choices, 105.  The gradient reads and writes: of the whole
+// softmax, 65536 x 256 bf16, 17-18 us (71 MB, 4.2 TB/s, partly from the Infinity
+// Cache), 65536 x 1024 fp32 119 (4.5); renormalised sigmoids 65536 x 256 fp32 19.4
+// (3.8), x 1024 76 (3.6, the row passes through 64 KB of LDS a workgroup).
 #include "elems.h"
 
 #include <cfloat>
@@ -175,8 +181,8 @@ __device__ __forceinline__ int32_t choose(const RouteArgs &a, const char *row, d
 
 // Scores of the chosen experts among themselves: lane j's score over the sum of
 // the token's, or the score itself.  mine: the lane's logit, -inf beside none;
-// most: the largest of them; low: below it sigmoids are taken relative to it,
-// so that they do not vanish, s_j / s_max = e^(l_j - m) (1 + e^m) / (1 + e^l_j).
+// most: the largest of them.  Where that is not above 0 sigmoids are taken relative
+// to its own, so that they do not vanish: s_j / s_max = e^(l_j - m) (1 + e^m) / (1 + e^l_j).
 __device__ __forceinline__ float part_of_score(int32_t score, float mine, float most) {
     if (!(mine > -INFINITY)) return 0.0f;
     if (score == OPTIM_ROUTE_SOFTMAX) return expf(mine - most);
@@ -437,9 +443,10 @@ __device__ __forceinline__ uint32_t pick(const uint32_t (&x)[N], int at) {
 //
 // Error of a choice c = s + b, in units of 2^-24: a sigmoid 1 / (1 + 2^(-l log2 e))
 // has s (1 - s) (1.22 |l| + 2) < 0.8 from the exponent and the exponential, 3 s from
-// the sum and the reciprocal, below 4; a softmax has its terms' |x| + 3, the sum's
-// V + 4 roundings one after another (V <= 64) and the terms' mean |x| + 3, and 3
-// of itself, below (V + 32) s as |x| e^-x < 1; the sum with b |c|.
+// the sum and the reciprocal, below 4; a softmax has its terms' 2.3 |x| + 3, the sum's
+// V + 4 roundings one after another (V <= 64) and the terms' mean 2.3 |x| + 3, and 3
+// of itself, below V + 32 of the largest score, as e^-|x| (2.3 |x| + 3) <= 3 and the
+// mean of |x| over 1024 terms e^-|x| with a 1 among them is below 4.5; the sum with b |c|.
 template <int V, int D, int DT, bool FULL>
 __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, Lay lay) {
     constexpr int V64 = V < 4 ? 1 : V / 4;

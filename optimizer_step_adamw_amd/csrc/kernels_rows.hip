@@ -8,14 +8,17 @@
 // expert, and the wavefront's count so far from LDS: no atomics on anything whose
 // order could show, and none that many lanes would meet in where one expert is
 // far more popular.  (The loops are loops: a workgroup goes through this code
-// once, and would wait for more of it to be fetched.)  Where one workgroup takes all, one launch counts, scans and
-// places; otherwise a first launch counts each chunk, and every workgroup of the
-// second sums what lies before its chunk.
+// once, and would wait for more of it to be fetched.)  Where one workgroup takes
+// all, one launch counts, scans and places; otherwise a first launch counts each
+// chunk, and every workgroup of the second sums what lies before its chunk.
 //
-// Bound by latency, two launches' chains of dependent steps: 65536 x 8 choices of
-// 256 experts 16.4 us (6 MB; the second launch, of which reading the choices and
-// the counts takes a third, ranks another), 4096 x 8 12.9, 1024 x 8 in one launch
-// 11-12, 300 x 2 4.5.
+// Bound by latency, two launches' chains of dependent steps.  Kernels' times in a
+// trace, us: 65536 x 8 choices of 256 experts 6.2 and 13.0 (6 MB; of the second one
+// reading the choices and the counts takes a third, ranks another), 4096 x 8 of 64
+// 3.1 and 8.6; in one launch 1024 x 8 11.6, 256 x 8 6.6, 300 x 2 of 8 4.5.  The
+// bias' step behind them 1.4, 4.0 for 256 experts.  Replayed from a graph, where a
+// launch begins while the one before ends, all three take 20.1 for 65536 x 8.  The
+// tables are as large for 8 experts as for 1024: one workgroup a CU.
 #include "device_common.h"
 #include "experts.h"
 
@@ -276,7 +279,7 @@ hipError_t launch_rows_t(const RowsArgs &args, hipStream_t s) {
 // One workgroup up to 8192 choices, then 128 of them (each of which reads the
 // counts of all), more once each has kHeld, and 512 at most.
 RowsShape rows_shape(int64_t n) {
-        int64_t chunk = n <= 8192 ? 8192 : std::max<int64_t>({n / 512, std::min<int64_t>(n / 128, kHeld), 4096});
+    int64_t chunk = n <= 8192 ? 8192 : std::max<int64_t>({n / 512, std::min<int64_t>(n / 128, kHeld), 4096});
     chunk += kRowLanes - 1;
     chunk -= chunk % kRowLanes;
     return RowsShape{(int32_t)chunk, (int32_t)((n + chunk - 1) / chunk)};

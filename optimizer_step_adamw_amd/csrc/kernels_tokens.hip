@@ -9,11 +9,12 @@
 // are a lane's own, in the order of its choices; the weights' gradients are joined
 // over the lanes in a fixed order.
 //
-// Bound by HBM.  Measured on MI355X: gather 16384 x 2048 bf16 to 8 rows each 115 us
-// (604 MB, 5.3 TB/s), combination of 16384 x 4096 bf16 from 2 with residual and
-// dropout 95-99 us (537 MB, 5.5), its gradient for 20001 x 1000 fp16 from 4 69 us
-// (361 MB, 5.2; 104 when each row was asked for behind the one before it); one
-// token of 4096 from 8 3.3 us.
+// Bound by HBM.  Measured on MI355X: gather 16384 x 2048 bf16 to 8 rows each 114-115
+// us (604 MB, 5.3 TB/s), combination of 16384 x 4096 bf16 from 2 with residual and
+// dropout 90-97 us (537 MB, 5.5-6.0; 103 at most in a trace), its gradient for 20001
+// x 1000 fp16 from 4 63-72 us (361 MB, 5.0-5.8; 104 when each row was asked for
+// behind the one before it), for 16384 x 2048 from 8, with dropout, bf16 236 us (4.8)
+// and fp32 440 (5.2); one token of 4096 from 8 3.3 us.
 #include "elems.h"
 
 namespace optim {
@@ -104,7 +105,10 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(TokenArgs a, int lp) 
     }
 }
 
-// J choices at a time: their dot products stay in registers over the columns.
+// J choices at a time: their dot products stay in registers over the columns.  More
+// than J choices, 8 at most, are rounds, each of which reads dout and draws the mask
+// again: 8192 x 2048 from 16, with dropout, bf16 242 us (4.6 TB/s of what it cannot do
+// without), fp32 469 (4.7).
 // `lp`: 1 << lp lanes a token, at most a workgroup, going over its chunks.
 template <int J, int DT, bool DROP>
 __global__ __launch_bounds__(kThreads) void combine_grad_kernel(TokenArgs a, int lp) {
