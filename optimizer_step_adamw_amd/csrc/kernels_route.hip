@@ -840,6 +840,8 @@ __global__ __launch_bounds__(kThreads) void route_grad_kernel(RouteGradArgs a) {
     wave_sync();
     float d;             // of the chosen expert, beside the row's own
     float x[C][8];       // the row's own
+    float of_top = 0.0f; // the same of an expert with more than half of the score (top)
+    bool top = false;
     if constexpr (WHOLE) {
         float most = -INFINITY, total = 0.0f;
 #pragma unroll
@@ -868,36 +870,33 @@ __global__ __launch_bounds__(kThreads) void route_grad_kernel(RouteGradArgs a) {
         const float by = -(lanes_sum<L>(d) * inv);
         // More than half of the score is one expert's, the only one whose term is 1: its
         // s (g - sum of g s) would be a difference of nearly equal numbers, and is
-        // s (g (1 - s) - sum over the others of g s), 1 - s from their terms.
-        const bool top = mine == from && s > 0.5f;
+        // s (g (1 - s) - sum over the others of g s), 1 - s from their terms (what is left
+        // of each without whole ones).  Where every row has such an expert that costs,
+        // measured, 65536 x 256 bf16 17.5 us for 17.0, x 1024 fp32 120 for 118.
+        top = mine == from && s > 0.5f;
         if (__any(top)) {
             float rest = 0.0f;
 #pragma unroll
             for (int i = 0; i < C; ++i)
 #pragma unroll
-                for (int v = 0; v < 8; ++v) rest += x[i][v] < 1.0f ? x[i][v] : 0.0f;
+                for (int v = 0; v < 8; ++v) rest += __builtin_amdgcn_fractf(x[i][v]);
             rest = lanes_sum<L>(rest);
-            const float by_top = lanes_max<L>(top ? 1.0f : 0.0f) > 0.0f ? -(lanes_sum<L>(top ? 0.0f : d) * inv) : by;
+            of_top = -(lanes_sum<L>(top ? 0.0f : d) * inv);
             d = top ? d * (rest * inv) : d;
-#pragma unroll
-            for (int i = 0; i < C; ++i)
-#pragma unroll
-                for (int v = 0; v < 8; ++v) x[i][v] = x[i][v] * (x[i][v] < 1.0f ? by : by_top);
-        } else {
-#pragma unroll
-            for (int i = 0; i < C; ++i)
-#pragma unroll
-                for (int v = 0; v < 8; ++v) x[i][v] = x[i][v] * by;
         }
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+#pragma unroll
+            for (int v = 0; v < 8; ++v) x[i][v] = x[i][v] * by;
     } else if (a.renormalise) {
         const float s = part_of_score(a.score, mine, lanes_max<L>(mine));
         const float total = lanes_sum<L>(s);
         const float w = total > 0.0f ? s / total : 0.0f;
         d = w * (g - lanes_sum<L>(g * w));
-        const bool top = w > 0.5f;  // (as above; one lane at most)
-        if (__any(top)) {
-            const float rest = lanes_sum<L>(top ? 0.0f : s), others = lanes_sum<L>(top ? 0.0f : g * w);
-            d = top ? w * (g * (rest / total) - others) : d;
+        const bool most = w > 0.5f;  // (as above; one lane at most)
+        if (__any(most)) {
+            const float rest = lanes_sum<L>(most ? 0.0f : s), others = lanes_sum<L>(most ? 0.0f : g * w);
+            d = most ? w * (g * (rest / total) - others) : d;
         }
         if (a.score == OPTIM_ROUTE_SIGMOID) d = d * sigmoid(-mine);
     } else {
@@ -924,7 +923,7 @@ __global__ __launch_bounds__(kThreads) void route_grad_kernel(RouteGradArgs a) {
         to[1] = WHOLE ? f32x4{x[i][4], x[i][5], x[i][6], x[i][7]} : zero;
     }
     wave_sync();
-    if (first) grad[e] += d;
+    if (first) grad[e] = (top ? of_top : grad[e]) + d;
     wave_sync();
     if (!live) return;
 #pragma unroll
